@@ -36,6 +36,9 @@ EXPORTED = (
     "mla_quantize_rows_fp8", "mla_decode_attn_fp8", "mla_selftest_wait_timeout",
     "mla_set_strict", "mla_decode_attn_range", "mla_combine_splits_f32", "mla_merge_ranges",
     "mla_combine_out_proj", "mla_plan_pieces_tiled", "mla_plan_tile",
+    "mla_cache_append_tree", "mla_tree_workspace_size", "mla_tree_attn", "mla_tree_accept",
+    "mla_block_keys", "mla_block_scores_workspace_size", "mla_block_scores", "mla_block_select",
+    "mla_decode_attn_sparse",
 )
 
 
@@ -96,6 +99,15 @@ def load(path: str | None = None) -> ctypes.CDLL:
         "mla_combine_out_proj": (i, [vp, vp, sz, i, i, vp, vp, vp, vp, vp, vp, vp]),
         "mla_plan_pieces_tiled": (ll, [vp, i, i, i, vp]),
         "mla_plan_tile": (i, [vp, i]),
+        "mla_cache_append_tree": (i, [vp, vp, i, i, vp, vp, vp, vp, vp, ll, vp, i, vp]),
+        "mla_tree_workspace_size": (i, [vp, i, i, i, ctypes.POINTER(sz)]),
+        "mla_tree_attn": (i, [vp, vp, vp, ll, vp, i, vp, vp, i, i, i, vp, vp, vp, sz, vp]),
+        "mla_tree_accept": (i, [vp, vp, ll, vp, i, vp, vp, vp, i, i, vp, vp]),
+        "mla_block_keys": (i, [vp, vp, ll, vp, i, vp, vp, i, i, vp, i, vp]),
+        "mla_block_scores_workspace_size": (i, [vp, i, i, ctypes.POINTER(sz)]),
+        "mla_block_scores": (i, [vp, vp, vp, i, vp, i, vp, vp, sz, vp]),
+        "mla_block_select": (i, [vp, vp, i, vp, i, i, i, i, vp, vp, vp]),
+        "mla_decode_attn_sparse": (i, [vp, vp, vp, ll, vp, i, vp, vp, vp, i, i, i, vp, sz, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -268,6 +280,67 @@ def mla_combine_out_proj(handle, workspace, ws_bytes, B, num_parts, w_uv, w_o, o
     _check(load().mla_combine_out_proj(handle, _ptr(workspace), ws_bytes, B, num_parts, _ptr(w_uv), _ptr(w_o),
                                        _ptr(o), _ptr(u), _ptr(ctx_lat), _ptr(lse), _stream(stream)),
            "mla_combine_out_proj")
+
+
+def mla_cache_append_tree(handle, h, B, T, ctx_len, depth, w_dkv, w_kr, cache, cache_len,
+                          block_table=None, max_blocks_per_seq=0, stream=None):
+    _check(load().mla_cache_append_tree(handle, _ptr(h), B, T, _ptr(ctx_len), _ptr(depth), _ptr(w_dkv),
+                                        _ptr(w_kr), _ptr(cache), cache_len, _ptr(block_table),
+                                        max_blocks_per_seq, _stream(stream)), "mla_cache_append_tree")
+
+
+def mla_tree_workspace_size(handle, B, T, num_parts=0) -> int:
+    n = ctypes.c_size_t()
+    _check(load().mla_tree_workspace_size(handle, B, T, num_parts, ctypes.byref(n)), "mla_tree_workspace_size")
+    return n.value
+
+
+def mla_tree_attn(handle, q_abs, cache, cache_len, block_table, max_blocks_per_seq, ctx_len, tree_mask, B, T,
+                  num_parts, ctx_lat, lse, workspace, ws_bytes, stream=None):
+    """tree_mask: int64 (or uint64) device tensor [B, T], bit j of word t = token t attends token j."""
+    _check(load().mla_tree_attn(handle, _ptr(q_abs), _ptr(cache), cache_len, _ptr(block_table),
+                                max_blocks_per_seq, _ptr(ctx_len), _ptr(tree_mask), B, T, num_parts,
+                                _ptr(ctx_lat), _ptr(lse), _ptr(workspace), ws_bytes, _stream(stream)),
+           "mla_tree_attn")
+
+
+def mla_tree_accept(handle, cache, cache_len, block_table, max_blocks_per_seq, ctx_len, path, n_path, B, T,
+                    new_len=None, stream=None):
+    _check(load().mla_tree_accept(handle, _ptr(cache), cache_len, _ptr(block_table), max_blocks_per_seq,
+                                  _ptr(ctx_len), _ptr(path), _ptr(n_path), B, T, _ptr(new_len),
+                                  _stream(stream)), "mla_tree_accept")
+
+
+def mla_block_keys(handle, cache, cache_len, block_table, max_blocks_per_seq, ctx_begin, ctx_len, B, max_new,
+                   keys, key_blocks, stream=None):
+    _check(load().mla_block_keys(handle, _ptr(cache), cache_len, _ptr(block_table), max_blocks_per_seq,
+                                 _ptr(ctx_begin), _ptr(ctx_len), B, max_new, _ptr(keys), key_blocks,
+                                 _stream(stream)), "mla_block_keys")
+
+
+def mla_block_scores_workspace_size(handle, B, key_blocks) -> int:
+    n = ctypes.c_size_t()
+    _check(load().mla_block_scores_workspace_size(handle, B, key_blocks, ctypes.byref(n)),
+           "mla_block_scores_workspace_size")
+    return n.value
+
+
+def mla_block_scores(handle, q_abs, keys, key_blocks, ctx_len, B, scores, workspace, ws_bytes, stream=None):
+    _check(load().mla_block_scores(handle, _ptr(q_abs), _ptr(keys), key_blocks, _ptr(ctx_len), B, _ptr(scores),
+                                   _ptr(workspace), ws_bytes, _stream(stream)), "mla_block_scores")
+
+
+def mla_block_select(handle, scores, key_blocks, ctx_len, B, k, n_first, n_last, sel, n_sel, stream=None):
+    _check(load().mla_block_select(handle, _ptr(scores), key_blocks, _ptr(ctx_len), B, k, n_first, n_last,
+                                   _ptr(sel), _ptr(n_sel), _stream(stream)), "mla_block_select")
+
+
+def mla_decode_attn_sparse(handle, q_abs, cache, cache_len, block_table, max_blocks_per_seq, ctx_len, sel, n_sel,
+                           k, B, num_parts, workspace, ws_bytes, stream=None):
+    _check(load().mla_decode_attn_sparse(handle, _ptr(q_abs), _ptr(cache), cache_len, _ptr(block_table),
+                                         max_blocks_per_seq, _ptr(ctx_len), _ptr(sel), _ptr(n_sel), k, B,
+                                         num_parts, _ptr(workspace), ws_bytes, _stream(stream)),
+           "mla_decode_attn_sparse")
 
 
 def mla_get_device_status(handle, stream=None) -> int:

@@ -3,6 +3,7 @@
 #include <stdlib.h>
 #include <string.h>
 
+#include <algorithm>
 #include <cmath>
 
 #include <nvtx3/nvToolsExt.h>
@@ -195,10 +196,11 @@ int mla_set_strict(mla_handle *h, int strict) {
   return MLA_OK;
 }
 
-int mla_cache_append(mla_handle *h, const void *x, int B, int T, const int *start_pos,
-                     const void *w_dkv, const void *w_kr, void *cache, long long cache_len,
-                     const int *block_table, int max_blocks_per_seq, mla_stream_t stream) {
-  Range range("mla_cache_append");
+namespace {
+// Cache append; depth NULL: a token is rotated by its own position.
+int cache_append(mla_handle *h, const void *x, int B, int T, const int *start_pos, const int *depth,
+                 const void *w_dkv, const void *w_kr, void *cache, long long cache_len,
+                 const int *block_table, int max_blocks_per_seq, mla_stream_t stream) {
   if (!h || B < 0 || T < 0 || cache_len < 0) return MLA_ERR_INVALID_ARG;
   if (B == 0 || T == 0) return MLA_OK;
   if (!x || !start_pos || !w_dkv || !w_kr || !cache) return MLA_ERR_INVALID_ARG;
@@ -209,13 +211,31 @@ int mla_cache_append(mla_handle *h, const void *x, int B, int T, const int *star
   cudaError_t e = cudaErrorNotSupported;
   if (h->gemm_kind == kGemmTc)
     e = launch_append_tc(c, x, B, T, start_pos, w_dkv, w_kr, cache, cache_len, block_table,
-                         max_blocks_per_seq, h->d_theta, h->d_status, s);
+                         max_blocks_per_seq, h->d_theta, h->d_status, s, nullptr, depth);
   if (strict_refuses(h, h->gemm_kind == kGemmTc, e)) return MLA_ERR_UNSUPPORTED;
   if (e == cudaErrorNotSupported)
     e = launch_append_simt(c, x, B, T, start_pos, w_dkv, w_kr, cache, cache_len, block_table,
-                           max_blocks_per_seq, h->d_theta, h->d_status, s);
+                           max_blocks_per_seq, h->d_theta, h->d_status, s, nullptr, depth);
   if (e == cudaErrorNotSupported) return MLA_ERR_UNSUPPORTED;
   return from_cuda(e);
+}
+}  // namespace
+
+int mla_cache_append(mla_handle *h, const void *x, int B, int T, const int *start_pos,
+                     const void *w_dkv, const void *w_kr, void *cache, long long cache_len,
+                     const int *block_table, int max_blocks_per_seq, mla_stream_t stream) {
+  Range range("mla_cache_append");
+  return cache_append(h, x, B, T, start_pos, nullptr, w_dkv, w_kr, cache, cache_len, block_table,
+                      max_blocks_per_seq, stream);
+}
+
+int mla_cache_append_tree(mla_handle *h, const void *x, int B, int T, const int *ctx_len, const int *depth,
+                          const void *w_dkv, const void *w_kr, void *cache, long long cache_len,
+                          const int *block_table, int max_blocks_per_seq, mla_stream_t stream) {
+  Range range("mla_cache_append_tree");
+  if (!h || T > kTreeMaxDrafted || (!depth && B > 0 && T > 0)) return MLA_ERR_INVALID_ARG;
+  return cache_append(h, x, B, T, ctx_len, depth, w_dkv, w_kr, cache, cache_len, block_table, max_blocks_per_seq,
+                      stream);
 }
 
 int mla_absorb_q(mla_handle *h, const void *q_nope, const void *q_rope, const int *pos,
@@ -244,28 +264,39 @@ size_t mla_decode_workspace_size(const mla_handle *h, int B, int num_parts) {
 }
 
 namespace {
+// Tokens one sequence can address: the contiguous cache's capacity, or the
+// pages of its block-table row.
+long long token_cap(const mla_config &c, long long cache_len, int max_blocks_per_seq) {
+  const long long cap = c.page_size > 0 ? (long long)max_blocks_per_seq * c.page_size : cache_len;
+  return cap < 0x7fffffffLL ? cap : 0x7fffffffLL;
+}
+
+float scale_log2_of(const mla_handle *h) {
+  return (float)(1.4426950408889634 * h->score_mult / sqrt((double)(h->cfg.d_h + h->cfg.d_r)));
+}
+
+// The block table is there for a paged cache, and only for one.
+bool table_ok(const mla_config &c, const int *block_table, int max_blocks_per_seq) {
+  return c.page_size > 0 ? block_table && max_blocks_per_seq > 0 : !block_table;
+}
+
 // Decode attention over a cache in cfg.dtype (kv_scale NULL) or of FP8 codes
 // with their group scales.
 int decode_attn(mla_handle *h, const void *q_abs, const void *cache, const float *kv_scale,
-                long long cache_len, const int *block_table, int max_blocks_per_seq, const int *ctx_begin,
-                const int *ctx_len, int B, int num_parts, void *workspace, size_t ws_bytes,
-                mla_stream_t stream) {
+                long long cache_len, const int *block_table, int max_blocks_per_seq, const PlanSource &src,
+                int B, int num_parts, void *workspace, size_t ws_bytes, mla_stream_t stream) {
   if (!h || B < 0 || num_parts < 0 || cache_len < 0) return MLA_ERR_INVALID_ARG;
   if (B == 0) return MLA_OK;
-  if (!q_abs || !cache || !ctx_len) return MLA_ERR_INVALID_ARG;
+  if (!q_abs || !cache || !src.ctx_len) return MLA_ERR_INVALID_ARG;
   const mla_config &c = h->cfg;
-  if (c.page_size > 0 && (!block_table || max_blocks_per_seq <= 0)) return MLA_ERR_INVALID_ARG;
-  if (c.page_size == 0 && block_table) return MLA_ERR_INVALID_ARG;
+  if (!table_ok(c, block_table, max_blocks_per_seq)) return MLA_ERR_INVALID_ARG;
   const int P = num_parts == 0 ? default_parts(h) : num_parts;
   const WsLayout L = ws_layout(c, B, P);
   if (!workspace || ((uintptr_t)workspace & 255u) || ws_bytes < L.total) return MLA_ERR_WORKSPACE;
   cudaStream_t s = (cudaStream_t)stream;
-  // Tokens one sequence can address: the contiguous cache's capacity, or the
-  // pages of its block-table row.
-  const long long cap = c.page_size > 0 ? (long long)max_blocks_per_seq * c.page_size : cache_len;
-  const long long cap_i = cap < 0x7fffffffLL ? cap : 0x7fffffffLL;
   const int tile = plan_tile_of(h, kv_scale != nullptr);
-  cudaError_t e = launch_plan(ctx_begin, ctx_len, B, P, cap_i, tile, (char *)workspace, L, h->d_status, s);
+  cudaError_t e = launch_plan(src, B, P, token_cap(c, cache_len, max_blocks_per_seq), tile, (char *)workspace, L,
+                              h->d_status, s);
   if (e != cudaSuccess) return MLA_ERR_CUDA;
   AttnArgs a;
   a.q_abs = q_abs;
@@ -278,13 +309,15 @@ int decode_attn(mla_handle *h, const void *q_abs, const void *cache, const float
   a.n_h = c.n_h;
   a.d_c = c.d_c;
   a.d_r = c.d_r;
-  a.scale_log2 = (float)(1.4426950408889634 * h->score_mult / sqrt((double)(c.d_h + c.d_r)));
+  a.scale_log2 = scale_log2_of(h);
   a.kv_scale = kv_scale;
   a.n_groups = fp8_num_groups(c.d_c, c.d_r);
   a.ws = (char *)workspace;
   a.L = L;
   a.plan_tile = tile;
   a.status = h->d_status;
+  a.sel = src.sel;
+  a.sel_k = src.sel_k;
   e = cudaErrorNotSupported;
   if (h->attn_kind == kAttnTcPair && !kv_scale && aligned16(q_abs) && aligned16(cache))
     e = launch_attn_tc_pair(a, P, s);
@@ -302,7 +335,7 @@ int mla_decode_attn(mla_handle *h, const void *q_abs, const void *cache, long lo
                     const int *block_table, int max_blocks_per_seq, const int *ctx_len, int B,
                     int num_parts, void *workspace, size_t ws_bytes, mla_stream_t stream) {
   Range range("mla_decode_attn");
-  return decode_attn(h, q_abs, cache, nullptr, cache_len, block_table, max_blocks_per_seq, nullptr, ctx_len, B,
+  return decode_attn(h, q_abs, cache, nullptr, cache_len, block_table, max_blocks_per_seq, PlanSource{ctx_len}, B,
                      num_parts, workspace, ws_bytes, stream);
 }
 
@@ -312,7 +345,7 @@ int mla_decode_attn_fp8(mla_handle *h, const void *q_abs, const void *cache, con
                         mla_stream_t stream) {
   Range range("mla_decode_attn_fp8");
   if (!kv_scale && h && B > 0) return MLA_ERR_INVALID_ARG;
-  return decode_attn(h, q_abs, cache, kv_scale, cache_len, block_table, max_blocks_per_seq, nullptr, ctx_len, B,
+  return decode_attn(h, q_abs, cache, kv_scale, cache_len, block_table, max_blocks_per_seq, PlanSource{ctx_len}, B,
                      num_parts, workspace, ws_bytes, stream);
 }
 
@@ -321,8 +354,194 @@ int mla_decode_attn_range(mla_handle *h, const void *q_abs, const void *cache, l
                           int B, int num_parts, void *workspace, size_t ws_bytes, mla_stream_t stream) {
   Range range("mla_decode_attn_range");
   if (!ctx_begin && h && B > 0) return MLA_ERR_INVALID_ARG;
-  return decode_attn(h, q_abs, cache, nullptr, cache_len, block_table, max_blocks_per_seq, ctx_begin, ctx_len, B,
-                     num_parts, workspace, ws_bytes, stream);
+  return decode_attn(h, q_abs, cache, nullptr, cache_len, block_table, max_blocks_per_seq,
+                     PlanSource{ctx_len, ctx_begin}, B, num_parts, workspace, ws_bytes, stream);
+}
+
+int mla_decode_attn_sparse(mla_handle *h, const void *q_abs, const void *cache, long long cache_len,
+                           const int *block_table, int max_blocks_per_seq, const int *ctx_len, const int *sel,
+                           const int *n_sel, int k, int B, int num_parts, void *workspace, size_t ws_bytes,
+                           mla_stream_t stream) {
+  Range range("mla_decode_attn_sparse");
+  if (!h || k < 0 || k > kMaxSelected) return MLA_ERR_INVALID_ARG;
+  if (B > 0 && (k == 0 || !sel || !n_sel)) return MLA_ERR_INVALID_ARG;
+  if (h->cfg.page_size % kTile != 0) return MLA_ERR_UNSUPPORTED;   // a block's rows must be consecutive
+  PlanSource src{ctx_len};
+  src.sel = sel;
+  src.n_sel = n_sel;
+  src.sel_k = k;
+  return decode_attn(h, q_abs, cache, nullptr, cache_len, block_table, max_blocks_per_seq, src, B, num_parts,
+                     workspace, ws_bytes, stream);
+}
+
+namespace {
+// Tree attention on the tensor cores: the DeepSeek-V2 latent shapes in bf16,
+// any number of heads (the query rows of a sequence are cut into 128s).
+bool tree_tc(const mla_config &c) {
+  return c.dtype == MLA_BF16 && c.d_c == 512 && c.d_r == 64 && (c.page_size == 0 || c.page_size == kTile);
+}
+
+struct TreeShape {
+  int groups, group_rows, parts, tile;
+  long long plan_seqs;
+  WsLayout L;
+  size_t copy_off, total;
+};
+
+TreeShape tree_shape(const mla_handle *h, bool tc, int B, int T, int num_parts) {
+  const mla_config &c = h->cfg;
+  TreeShape t;
+  const long long rows = (long long)T * c.n_h;
+  t.group_rows = tc ? 128 : c.n_h;
+  t.groups = (int)ceil_div_ll(rows, t.group_rows);
+  t.parts = num_parts > 0 ? num_parts : (tc ? h->num_sms / 2 : h->num_sms * 4);
+  t.tile = tc ? 256 : kTile;
+  t.plan_seqs = (long long)B * t.groups;
+  if (t.plan_seqs > kMaxPlanSeqs) {
+    t.total = 0;
+    return t;
+  }
+  t.L = tree_ws_layout(t.group_rows, c.d_c, (int)t.plan_seqs, t.parts);
+  t.copy_off = t.L.total;
+  t.total = align_up(t.L.total + (tc ? tree_copy_bytes(B) : 0), 256);
+  return t;
+}
+}  // namespace
+
+int mla_tree_workspace_size(const mla_handle *h, int B, int T, int num_parts, size_t *bytes) {
+  if (!h || B < 0 || T < 0 || T > kTreeMaxDrafted || num_parts < 0 || !bytes) return MLA_ERR_INVALID_ARG;
+  const TreeShape simt = tree_shape(h, false, B, T, num_parts);
+  if (simt.total == 0) return MLA_ERR_UNSUPPORTED;
+  *bytes = simt.total;
+  if (tree_tc(h->cfg)) *bytes = std::max(*bytes, tree_shape(h, true, B, T, num_parts).total);   // either may run
+  return MLA_OK;
+}
+
+int mla_tree_attn(mla_handle *h, const void *q_abs, const void *cache, long long cache_len, const int *block_table,
+                  int max_blocks_per_seq, const int *ctx_len, const unsigned long long *tree_mask, int B, int T,
+                  int num_parts, void *ctx_lat, float *lse, void *workspace, size_t ws_bytes, mla_stream_t stream) {
+  Range range("mla_tree_attn");
+  if (!h || B < 0 || T < 0 || T > kTreeMaxDrafted || num_parts < 0 || cache_len < 0) return MLA_ERR_INVALID_ARG;
+  if (B == 0 || T == 0) return MLA_OK;
+  if (!q_abs || !cache || !ctx_len || !tree_mask || !ctx_lat) return MLA_ERR_INVALID_ARG;
+  const mla_config &c = h->cfg;
+  if (!table_ok(c, block_table, max_blocks_per_seq)) return MLA_ERR_INVALID_ARG;
+  size_t need = 0;
+  const int st = mla_tree_workspace_size(h, B, T, num_parts, &need);
+  if (st != MLA_OK) return st;
+  if (!workspace || ((uintptr_t)workspace & 255u) || ws_bytes < need) return MLA_ERR_WORKSPACE;
+  cudaStream_t s = (cudaStream_t)stream;
+  const long long cap = token_cap(c, cache_len, max_blocks_per_seq);
+  auto attend = [&](bool tc) -> cudaError_t {
+    const TreeShape t = tree_shape(h, tc, B, T, num_parts);
+    AttnArgs a = {};
+    a.q_abs = q_abs;
+    a.cache = cache;
+    a.cache_len = cache_len;
+    a.block_table = block_table;
+    a.max_blocks = max_blocks_per_seq;
+    a.page_size = c.page_size;
+    a.B = (int)t.plan_seqs;
+    a.n_h = c.n_h;
+    a.d_c = c.d_c;
+    a.d_r = c.d_r;
+    a.scale_log2 = scale_log2_of(h);
+    a.ws = (char *)workspace;
+    a.L = t.L;
+    a.plan_tile = t.tile;
+    a.status = h->d_status;
+    a.tree.T = T;
+    a.tree.groups = t.groups;
+    a.tree.group_rows = t.group_rows;
+    a.tree.seq_rows = T * c.n_h;
+    a.tree.mask = tree_mask;
+    a.tree.out = ctx_lat;
+    a.tree.lse = lse;
+    a.tree.copy_off = t.copy_off;
+    PlanSource src{ctx_len};
+    src.groups = t.groups;
+    src.drafted = T;
+    cudaError_t e;
+    if (tc) {
+      // the tensor maps are made before anything is launched
+      if (!aligned16(q_abs) || !aligned16(cache) || !aligned16(ctx_lat)) return cudaErrorNotSupported;
+      e = launch_tree_attn_tc_pair(a, t.parts, s, [&] { return launch_tree_plan_copy(src, a, t.parts, cap, s); });
+    } else {
+      e = launch_plan(src, a.B, t.parts, cap, t.tile, a.ws, a.L, a.status, s);
+      if (e == cudaSuccess) e = launch_tree_attn_simt(a, t.parts, c.dtype == MLA_FP32, s);
+    }
+    return e == cudaSuccess ? launch_tree_combine(a, t.parts, c.dtype == MLA_FP32, s) : e;
+  };
+  cudaError_t e = cudaErrorNotSupported;
+  if (tree_tc(c)) e = attend(true);
+  if (strict_refuses(h, tree_tc(c), e)) return MLA_ERR_UNSUPPORTED;
+  if (e == cudaErrorNotSupported) e = attend(false);
+  if (e == cudaErrorNotSupported) return MLA_ERR_UNSUPPORTED;
+  return from_cuda(e);
+}
+
+int mla_tree_accept(mla_handle *h, void *cache, long long cache_len, const int *block_table, int max_blocks_per_seq,
+                    const int *ctx_len, const int *path, const int *n_path, int B, int T, int *new_len,
+                    mla_stream_t stream) {
+  Range range("mla_tree_accept");
+  if (!h || B < 0 || T < 0 || T > kTreeMaxDrafted || cache_len < 0) return MLA_ERR_INVALID_ARG;
+  if (B == 0 || T == 0) return MLA_OK;
+  if (!cache || !ctx_len || !path || !n_path) return MLA_ERR_INVALID_ARG;
+  if (!table_ok(h->cfg, block_table, max_blocks_per_seq)) return MLA_ERR_INVALID_ARG;
+  const cudaError_t e = launch_tree_accept(h->cfg, cache, cache_len, block_table, max_blocks_per_seq, ctx_len, path,
+                                           n_path, B, T, new_len, h->d_status, (cudaStream_t)stream);
+  return e == cudaErrorNotSupported ? MLA_ERR_UNSUPPORTED : from_cuda(e);
+}
+
+int mla_block_keys(mla_handle *h, const void *cache, long long cache_len, const int *block_table,
+                   int max_blocks_per_seq, const int *ctx_begin, const int *ctx_len, int B, int max_new, void *keys,
+                   int key_blocks, mla_stream_t stream) {
+  Range range("mla_block_keys");
+  if (!h || B < 0 || max_new < 0 || key_blocks < 0 || cache_len < 0) return MLA_ERR_INVALID_ARG;
+  if (B == 0 || max_new == 0) return MLA_OK;
+  if (!cache || !ctx_len || !keys || key_blocks == 0) return MLA_ERR_INVALID_ARG;
+  if (!table_ok(h->cfg, block_table, max_blocks_per_seq)) return MLA_ERR_INVALID_ARG;
+  const cudaError_t e = launch_block_keys(h->cfg, cache, cache_len, block_table, max_blocks_per_seq, ctx_begin,
+                                          ctx_len, B, max_new, keys, key_blocks, h->d_status, (cudaStream_t)stream);
+  return e == cudaErrorNotSupported ? MLA_ERR_UNSUPPORTED : from_cuda(e);
+}
+
+int mla_block_scores_workspace_size(const mla_handle *h, int B, int key_blocks, size_t *bytes) {
+  if (!h || B < 0 || key_blocks < 0 || !bytes) return MLA_ERR_INVALID_ARG;
+  *bytes = score_layout(h->cfg, B, key_blocks).total;
+  return MLA_OK;
+}
+
+int mla_block_scores(mla_handle *h, const void *q_abs, const void *keys, int key_blocks, const int *ctx_len, int B,
+                     float *scores, void *workspace, size_t ws_bytes, mla_stream_t stream) {
+  Range range("mla_block_scores");
+  if (!h || B < 0 || key_blocks < 0) return MLA_ERR_INVALID_ARG;
+  if (B == 0 || key_blocks == 0) return MLA_OK;
+  if (!q_abs || !keys || !ctx_len || !scores) return MLA_ERR_INVALID_ARG;
+  const ScoreLayout L = score_layout(h->cfg, B, key_blocks);
+  if (!workspace || ((uintptr_t)workspace & 255u) || ws_bytes < L.total) return MLA_ERR_WORKSPACE;
+  const bool tc = h->cfg.dtype == MLA_BF16 && h->cfg.d_c == 512 && h->cfg.d_r == 64;
+  cudaError_t e = cudaErrorNotSupported;
+  if (tc)
+    e = launch_block_scores(h->cfg, true, scale_log2_of(h), q_abs, keys, key_blocks, ctx_len, B, scores,
+                            (char *)workspace, L, h->d_status, (cudaStream_t)stream);
+  if (strict_refuses(h, tc, e)) return MLA_ERR_UNSUPPORTED;
+  if (e == cudaErrorNotSupported)
+    e = launch_block_scores(h->cfg, false, scale_log2_of(h), q_abs, keys, key_blocks, ctx_len, B, scores,
+                            (char *)workspace, L, h->d_status, (cudaStream_t)stream);
+  return e == cudaErrorNotSupported ? MLA_ERR_UNSUPPORTED : from_cuda(e);
+}
+
+int mla_block_select(mla_handle *h, const float *scores, int key_blocks, const int *ctx_len, int B, int k, int n_first,
+                     int n_last, int *sel, int *n_sel, mla_stream_t stream) {
+  Range range("mla_block_select");
+  if (!h || B < 0 || key_blocks < 0 || k < 0 || k > kMaxSelected || n_first < 0 || n_last < 0)
+    return MLA_ERR_INVALID_ARG;
+  if (B == 0) return MLA_OK;
+  if (!ctx_len || !n_sel || (key_blocks > 0 && !scores) || (k > 0 && !sel)) return MLA_ERR_INVALID_ARG;
+  const cudaError_t e = launch_block_select(scores, key_blocks, ctx_len, B, k, n_first, n_last, sel, n_sel,
+                                            h->d_status, (cudaStream_t)stream);
+  return e == cudaErrorNotSupported ? MLA_ERR_UNSUPPORTED : from_cuda(e);
 }
 
 int mla_fp8_scale_groups(const mla_handle *h) { return h ? fp8_num_groups(h->cfg.d_c, h->cfg.d_r) : 0; }

@@ -6,7 +6,9 @@
 #include <cuda_bf16.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <atomic>
+#include <functional>
 #include <mutex>
 
 #include "mla.h"
@@ -142,6 +144,19 @@ __host__ __device__ inline long long plan_share_of_tile(long long t, long long P
 }
 __host__ __device__ inline long long ceil_div_ll(long long a, long long b) { return (a + b - 1) / b; }
 
+// What the plan cuts into tiles.  A plan sequence is one of `groups` row groups
+// of a batch sequence (1 except for a tree of drafted tokens, whose query rows
+// are cut into groups; plan sequence v belongs to batch sequence v / groups).
+struct PlanSource {
+  const int *ctx_len;              // [B] cached tokens
+  const int *ctx_begin = nullptr;  // [B] first attended token, or NULL (0)
+  int groups = 1;
+  int drafted = 0;                 // tree: drafted tokens behind the ctx_len cached ones
+  const int *sel = nullptr;        // selected blocks [B, sel_k], or NULL (every block)
+  const int *n_sel = nullptr;      // [B] how many of them
+  int sel_k = 0;
+};
+
 // Workspace header written by the plan kernel; the per-sequence arrays follow.
 struct WsHeader {
   long long B;
@@ -153,7 +168,8 @@ struct WsHeader {
 struct WsLayout {
   size_t tile_prefix_off;  // int64 [B+1]
   size_t piece_base_off;   // int64 [B+1]
-  size_t ctx_off;          // int32 [2][B]: each sequence's end and first token as attended (clamped by the plan)
+  size_t ctx_off;          // int32 [2][B]: each sequence's end as attended (clamped by the plan), and its first token
+                           // (selected blocks and trees: its cached tokens instead; they start at token 0)
   size_t share_first_off;  // int32 [P]: the first sequence whose tiles reach into each share
   size_t opart_off;        // float [n_h, max_pieces, d_c]: a head's pieces are consecutive rows
   size_t lse_off;          // float [n_h, max_pieces]
@@ -169,9 +185,11 @@ __host__ __device__ inline long long part_row(const WsLayout &L, long long piece
   return (long long)head * L.max_pieces + piece;
 }
 
-inline WsLayout ws_layout(const mla_config &cfg, int B, int P) {
+// Layout for B plan sequences of `rows` query rows each, P shares and room for
+// `pieces` pieces.
+inline WsLayout ws_layout_rows(int rows, int d_c, int B, int P, long long pieces) {
   WsLayout L;
-  L.max_pieces = (long long)P + B;
+  L.max_pieces = pieces;
   size_t off = align_up(sizeof(WsHeader), 256);
   L.tile_prefix_off = off;
   off = align_up(off + sizeof(long long) * (size_t)(B + 1), 256);
@@ -182,12 +200,47 @@ inline WsLayout ws_layout(const mla_config &cfg, int B, int P) {
   L.share_first_off = off;
   off = align_up(off + sizeof(int) * (size_t)(P > 0 ? P : 1), 256);
   L.opart_off = off;
-  off = align_up(off + sizeof(float) * (size_t)L.max_pieces * cfg.n_h * cfg.d_c, 256);
+  off = align_up(off + sizeof(float) * (size_t)L.max_pieces * rows * d_c, 256);
   L.lse_off = off;
-  off = align_up(off + sizeof(float) * (size_t)L.max_pieces * cfg.n_h, 256);
+  off = align_up(off + sizeof(float) * (size_t)L.max_pieces * rows, 256);
   L.total = off;
   return L;
 }
+
+inline WsLayout ws_layout(const mla_config &cfg, int B, int P) {
+  return ws_layout_rows(cfg.n_h, cfg.d_c, B, P, (long long)P + B);
+}
+
+// Tree attention: the query rows (drafted token, head) of a sequence are cut
+// into groups of `rows`, each a plan sequence.  Only a group that is split
+// between shares leaves partials, and a share holds at most two such pieces
+// (its first and its last), which take slots 2w and 2w + 1 of the 2 P.
+inline WsLayout tree_ws_layout(int rows, int d_c, int plan_seqs, int P) {
+  return ws_layout_rows(rows, d_c, plan_seqs, P, 2ll * P);
+}
+
+// The tensor-core kernel reads the blocks that hold drafted tokens, the last
+// partial block of the cached ones with them, from a copy of at most two
+// blocks per sequence behind the partials: bf16 [batch, kTreeCopyRows, 576],
+// zeros past the drafted tokens, non-finite values of drafted tokens zero.
+constexpr int kTreeCopyRows = 2 * kTile;
+constexpr int kTreeMaxDrafted = 64;   // a tree's masks are 64-bit words
+constexpr int kMaxPlanSeqs = 1 << 24; // row groups of one call (the plan's arrays and prefix sums)
+constexpr int kMaxSelected = 1 << 20; // selected blocks per sequence
+inline size_t tree_copy_bytes(int batch) { return (size_t)batch * kTreeCopyRows * 576 * 2; }
+
+// Tree of drafted tokens: the query rows of sequence b are (t, head), t
+// outermost, T * n_h of them in `groups` groups of `group_rows`; drafted token
+// t sits in cache slot cached + t and attends every cached token and the
+// drafted ones whose bit is set in mask[b, t].
+struct TreeArgs {
+  int T = 0;                                // 0: no tree
+  int groups = 1, group_rows = 0, seq_rows = 0;
+  const unsigned long long *mask = nullptr; // [batch, T]
+  void *out = nullptr;                      // [batch, T, n_h, d_c], the cache's dtype
+  float *lse = nullptr;                     // [batch, T, n_h] or NULL
+  size_t copy_off = 0;                      // tensor-core kernel: offset of the copied blocks in the workspace
+};
 
 // Arguments shared by the attention kernels.
 struct AttnArgs {
@@ -208,6 +261,11 @@ struct AttnArgs {
   WsLayout L;
   int plan_tile;     // tokens per tile of the split plan
   unsigned *status;
+  // Selected blocks [B, sel_k] of 64 tokens (NULL: every block): token t of a
+  // sequence is then token t % 64 of its block sel[b, t / 64].
+  const int *sel = nullptr;
+  int sel_k = 0;
+  TreeArgs tree;     // B is then the number of plan sequences (groups x batch)
 };
 
 // ---------------------------------------------------------------------------
@@ -221,22 +279,98 @@ struct AttnArgs {
 // attention kernel reads those instead of the caller's arrays, so that the
 // plan's tiles and the kernels' token ranges agree.  `tile` (a multiple of
 // kTile) is the plan's tile in tokens.
-cudaError_t launch_plan(const int *ctx_begin, const int *ctx_len, int B, int P, long long cap, int tile, char *ws,
-                        const WsLayout &L, unsigned *status, cudaStream_t s);
+// With a tree the plan attends the cached tokens and the drafted ones behind
+// them (clamped to cap); with selected blocks the tokens of those blocks, the
+// last of which may be the sequence's partial one.
+cudaError_t launch_plan(const PlanSource &src, int B, int P, long long cap, int tile, char *ws, const WsLayout &L,
+                        unsigned *status, cudaStream_t s);
+
+// The plan of a tree for the tensor-core kernel, and in the same launch the
+// copy of the blocks that hold drafted tokens (a: every field but the plan's).
+cudaError_t launch_tree_plan_copy(const PlanSource &src, const AttnArgs &a, int P, long long cap, cudaStream_t s);
 
 // The clamped end (context length) of sequence b, as the plan stored it.
 __device__ __forceinline__ int plan_ctx(const char *ws, const WsLayout &L, int b) {
   return reinterpret_cast<const int *>(ws + L.ctx_off)[b];
 }
 // The first attended token of sequence b (a multiple of kTile).
-__device__ __forceinline__ int plan_begin_tok(const char *ws, const WsLayout &L, int b, int B) {
-  return reinterpret_cast<const int *>(ws + L.ctx_off)[B + b];
+__device__ __forceinline__ int plan_begin_tok(const AttnArgs &a, int b) {
+  if (a.sel || a.tree.T) return 0;
+  return reinterpret_cast<const int *>(a.ws + a.L.ctx_off)[a.B + b];
+}
+// The cached tokens of plan sequence b (selected blocks and trees).
+__device__ __forceinline__ int plan_cached(const AttnArgs &a, int b) {
+  return reinterpret_cast<const int *>(a.ws + a.L.ctx_off)[a.B + b];
+}
+
+// Cache row of token t of batch sequence b (t below what the cache can
+// address), or -1 when its page is unmapped or outside the pool.
+__device__ __forceinline__ long long token_row(const AttnArgs &a, int b, long long t) {
+  if (a.page_size == 0) return t < a.cache_len ? (long long)b * a.cache_len + t : -1;
+  const long long bi = t / a.page_size;
+  if (bi >= a.max_blocks) return -1;
+  const int blk = a.block_table[(long long)b * a.max_blocks + bi];
+  if (blk < 0 || blk >= a.cache_len) return -1;
+  return (long long)blk * a.page_size + t % a.page_size;
+}
+
+// The same for token t of a sequence's selected blocks.  -1 also for a block
+// that the sequence does not have, and for its partial last block anywhere
+// but at the end of the selection (end: the selected tokens).
+__device__ __forceinline__ long long selected_row(const AttnArgs &a, int b, long long t, int end) {
+  const int blk = a.sel[(long long)b * a.sel_k + t / kTile];
+  const int cached = plan_cached(a, b);
+  if (blk < 0 || (long long)blk * kTile >= cached) return -1;
+  if (((long long)blk + 1) * kTile > cached && t / kTile != (end - 1) / kTile) return -1;
+  return token_row(a, b, (long long)blk * kTile + t % kTile);
+}
+
+// How a piece of tree attention ends.  A group whose tiles all lie in one
+// share is written out at once; a part of a split group leaves a partial in
+// one of its share's two slots.
+struct TreePiece {
+  bool whole;
+  long long slot;
+};
+__device__ __forceinline__ TreePiece tree_piece(const long long *tile_prefix, int v, long long w, long long P,
+                                                long long Ttot) {
+  const long long s0 = tile_prefix[v], s1 = tile_prefix[v + 1];
+  const long long t0 = plan_begin(w, P, Ttot), t1 = plan_begin(w + 1, P, Ttot);
+  return {s0 >= t0 && s1 <= t1, 2 * w + (s0 > t0 ? 1 : 0)};
 }
 
 cudaError_t launch_attn_simt(const AttnArgs &a, int P, bool fp32, cudaStream_t s);
+cudaError_t launch_tree_attn_simt(const AttnArgs &a, int P, bool fp32, cudaStream_t s);
 // With out_f32, ctx_lat is written in float32 whatever cfg.dtype.
 cudaError_t launch_combine(const mla_config &cfg, const char *ws, const WsLayout &L, int B,
                            void *ctx_lat, float *lse, cudaStream_t s, bool out_f32 = false);
+// Tree attention: merge of the groups that are split between shares, straight
+// into the outputs (in P x group_rows warps; the other groups are there already).
+cudaError_t launch_tree_combine(const AttnArgs &a, int P, bool fp32, cudaStream_t s);
+// Accepted path of a drafted tree: row ctx_len[b] + path[b, i] of the cache
+// moves to ctx_len[b] + i, i < n_path[b]; new_len[b] = ctx_len[b] + n_path[b].
+cudaError_t launch_tree_accept(const mla_config &cfg, void *cache, long long cache_len, const int *block_table,
+                               int max_blocks, const int *ctx_len, const int *path, const int *n_path, int B, int T,
+                               int *new_len, unsigned *status, cudaStream_t s);
+
+// Selection of cached blocks (blocks.cu).
+cudaError_t launch_block_keys(const mla_config &cfg, const void *cache, long long cache_len, const int *block_table,
+                              int max_blocks, const int *ctx_begin, const int *ctx_len, int B, int max_new, void *keys,
+                              int key_blocks, unsigned *status, cudaStream_t s);
+struct ScoreLayout {
+  size_t logit_off;   // float [B, head_rows, blocks rounded up to 128]
+  size_t stat_off;    // float2 [B, block tiles, head_rows]: a tile's maximum and sum of exponentials
+  size_t total;
+  int head_rows;      // heads rounded up to 128
+  int tiles;          // 128-block tiles
+};
+ScoreLayout score_layout(const mla_config &cfg, int B, int key_blocks);
+cudaError_t launch_block_scores(const mla_config &cfg, bool tc, float scale_log2, const void *q_abs, const void *keys,
+                                int key_blocks, const int *ctx_len, int B, float *scores, char *ws,
+                                const ScoreLayout &L, unsigned *status, cudaStream_t s);
+cudaError_t launch_block_select(const float *scores, int n_blocks, const int *ctx_len, int B, int k, int n_first,
+                                int n_last, int *sel, int *n_sel, unsigned *status, cudaStream_t s);
+
 // Merge of R float32 token-range results [R, B, n_h, d_c] with their
 // log-sum-exps [R, B, n_h] into ctx_lat [B, n_h, d_c] (cfg.dtype) and lse.
 cudaError_t launch_merge_ranges(const mla_config &cfg, const float *parts, const float *lse_parts, int R, int B,
@@ -246,7 +380,7 @@ cudaError_t launch_append_simt(const mla_config &cfg, const void *h, int B, int 
                                const int *start_pos, const void *w_dkv, const void *w_kr,
                                void *cache, long long cache_len, const int *block_table,
                                int max_blocks, const double *theta, unsigned *status,
-                               cudaStream_t s, float *rows_out = nullptr);
+                               cudaStream_t s, float *rows_out = nullptr, const int *depth = nullptr);
 // FP8 E4M3 quantisation of n_rows rows [n_rows, d_c + d_r] (cfg.dtype, or
 // float32 when src_f32): per row and 128-channel group, sigma = amax / 448 and
 // codes E4M3(x / sigma).  With start_pos, row r is token r % T of sequence
@@ -270,13 +404,15 @@ cudaError_t launch_linear_simt(const void *x, const void *w, void *y, int M, int
                                cudaStream_t s);
 
 // tcgen05 paths (bf16 only); return cudaErrorNotSupported for shapes they lack.
+// With depth [B, T] set, token t of sequence b is rotated by position
+// start_pos[b] + depth[b, t] (its slot stays start_pos[b] + t).
 // With rows_out set, the rotated rows go to rows_out [B*T, d_c + d_r] in
 // float32 instead of to the cache (the cache arguments are then unused).
 cudaError_t launch_append_tc(const mla_config &cfg, const void *h, int B, int T,
                              const int *start_pos, const void *w_dkv, const void *w_kr,
                              void *cache, long long cache_len, const int *block_table,
                              int max_blocks, const double *theta, unsigned *status,
-                             cudaStream_t s, float *rows_out = nullptr);
+                             cudaStream_t s, float *rows_out = nullptr, const int *depth = nullptr);
 cudaError_t launch_absorb_tc(const mla_config &cfg, const void *q_nope, const void *q_rope,
                              const int *pos, const void *w_uk, void *q_abs, int B,
                              const double *theta, unsigned *status, cudaStream_t s);
@@ -293,6 +429,11 @@ cudaError_t launch_combine_outproj_tc(const mla_config &cfg, const char *ws, con
                                       const void *w_uv, void *o, void *ctx_lat, float *lse, unsigned *status,
                                       cudaStream_t s);
 cudaError_t launch_attn_tc_pair(const AttnArgs &a, int P, cudaStream_t s);
+// The same kernel over a tree of drafted tokens, 128 query rows at a time.
+// `plan` launches what goes before it, once the arguments are known to be ones
+// it can take.
+cudaError_t launch_tree_attn_tc_pair(const AttnArgs &a, int P, cudaStream_t s,
+                                     const std::function<cudaError_t()> &plan);
 cudaError_t launch_attn_tc_smallh(const AttnArgs &a, int P, cudaStream_t s);
 
 // One bounded wait on a barrier that nothing completes, giving up after

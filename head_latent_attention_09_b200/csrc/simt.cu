@@ -73,11 +73,8 @@ __device__ long long block_exclusive_scan(long long v, long long *smem, long lon
   return before + x - v;
 }
 
-__global__ void __launch_bounds__(1024) plan_kernel(const int *ctx_begin, const int *ctx_len, int B, int P_req,
-                                                    long long cap, int tile, char *ws, WsLayout L,
-                                                    unsigned *status) {
-  pdl_trigger();
-  pdl_wait();   // the workspace may still be read by the previous step's combine
+__device__ void make_plan(const PlanSource &src, int B, int P_req, long long cap, int tile, char *ws,
+                          const WsLayout &L, unsigned *status) {
   __shared__ long long scan[32];
   long long *tile_prefix = reinterpret_cast<long long *>(ws + L.tile_prefix_off);
   long long *piece_base = reinterpret_cast<long long *>(ws + L.piece_base_off);
@@ -91,12 +88,40 @@ __global__ void __launch_bounds__(1024) plan_kernel(const int *ctx_begin, const 
   for (int b = b0; b < b1; ++b) {
     // A length outside [0, cap] is flagged and clamped; the tiles below and
     // every attention kernel use the clamped length.
-    long long c = ctx_len[b];
+    const int seq = src.groups > 1 ? b / src.groups : b;
+    long long c = src.ctx_len[seq];
     if (c < 0 || c > cap) {
       atomicOr(status, kStatusBounds);
       c = c < 0 ? 0 : cap;
     }
-    long long g = ctx_begin ? ctx_begin[b] : 0;
+    if (src.drafted > 0 || src.sel) {
+      // the second value kept is the number of cached tokens; the first token is 0
+      long long end;
+      if (src.sel) {
+        long long n = src.n_sel[seq];
+        const long long most = min((long long)src.sel_k, ceil_div_ll(c, kTile));
+        if (n < 0 || n > most) {
+          atomicOr(status, kStatusBounds);
+          n = n < 0 ? 0 : most;
+        }
+        end = n * kTile;
+        if (n > 0) {
+          const long long last = src.sel[(long long)seq * src.sel_k + n - 1];
+          if (last >= 0 && last * kTile < c) end -= max(0ll, (last + 1) * kTile - c);   // the partial block
+        }
+      } else {
+        end = c + src.drafted;
+        if (end > cap) {
+          atomicOr(status, kStatusBounds);
+          end = cap;
+        }
+      }
+      ctx_eff[b] = (int)end;
+      beg_eff[b] = (int)c;
+      local += ceil_div_ll(end, tile);
+      continue;
+    }
+    long long g = src.ctx_begin ? src.ctx_begin[b] : 0;
     if (g < 0 || g > c || g % kTile != 0) {
       atomicOr(status, kStatusBounds);
       g = g < 0 ? 0 : (g > c ? c : g);
@@ -106,11 +131,13 @@ __global__ void __launch_bounds__(1024) plan_kernel(const int *ctx_begin, const 
     beg_eff[b] = (int)g;
     local += ceil_div_ll(c - g, tile);
   }
+  const bool from0 = src.drafted > 0 || src.sel;
+  auto tiles_of = [&](int b) { return ceil_div_ll(ctx_eff[b] - (from0 ? 0 : beg_eff[b]), tile); };
   long long Ttot;
   long long run = block_exclusive_scan(local, scan, &Ttot);
   for (int b = b0; b < b1; ++b) {
     tile_prefix[b] = run;
-    run += ceil_div_ll(ctx_eff[b] - beg_eff[b], tile);
+    run += tiles_of(b);
   }
   if (tid == 0) tile_prefix[B] = Ttot;
   const long long P = Ttot < (long long)P_req ? Ttot : (long long)P_req;
@@ -118,7 +145,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(const int *ctx_begin, const 
   long long local_pieces = 0;
   for (int b = b0; b < b1; ++b) {
     long long s = tile_prefix[b];
-    long long t = ceil_div_ll(ctx_eff[b] - beg_eff[b], tile);
+    long long t = tiles_of(b);
     if (t > 0) local_pieces += plan_share_of_tile(s + t - 1, P, Ttot) - plan_share_of_tile(s, P, Ttot) + 1;
   }
   long long n_pieces;
@@ -126,7 +153,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(const int *ctx_begin, const 
   for (int b = b0; b < b1; ++b) {
     piece_base[b] = prun;
     long long s = tile_prefix[b];
-    long long t = ceil_div_ll(ctx_eff[b] - beg_eff[b], tile);
+    long long t = tiles_of(b);
     if (t > 0) prun += plan_share_of_tile(s + t - 1, P, Ttot) - plan_share_of_tile(s, P, Ttot) + 1;
   }
   // Each share's first sequence (the first whose tiles reach past the share's
@@ -149,7 +176,54 @@ __global__ void __launch_bounds__(1024) plan_kernel(const int *ctx_begin, const 
     hd->P = P;
     hd->Ttot = Ttot;
     hd->n_pieces = n_pieces;
-    if (n_pieces > L.max_pieces) atomicOr(status, kStatusBounds);  // cannot happen by construction
+    if (src.drafted == 0 && n_pieces > L.max_pieces) atomicOr(status, kStatusBounds);  // cannot happen by construction
+  }
+}
+
+__global__ void __launch_bounds__(1024) plan_kernel(PlanSource src, int B, int P_req, long long cap, int tile,
+                                                    char *ws, WsLayout L, unsigned *status) {
+  pdl_trigger();
+  pdl_wait();   // the workspace may still be read by the previous step's combine
+  make_plan(src, B, P_req, cap, tile, ws, L, status);
+}
+
+// Eight bf16 values with the non-finite ones replaced by zero.
+__device__ __forceinline__ uint4 finite_or_zero(uint4 v) {
+  auto one = [](uint32_t x) {
+    if ((x & 0x7f80u) == 0x7f80u) x &= 0xffff0000u;
+    if ((x & 0x7f800000u) == 0x7f800000u) x &= 0x0000ffffu;
+    return x;
+  };
+  return make_uint4(one(v.x), one(v.y), one(v.z), one(v.w));
+}
+
+// Tree: block 0 makes the plan while the others copy the blocks that hold
+// drafted tokens, kCopyBlocks blocks of kCopyRows rows per sequence (rows of
+// 72 16-byte units).
+constexpr int kCopyRows = 8, kCopyBlocks = kTreeCopyRows / kCopyRows;
+__global__ void __launch_bounds__(1024) tree_plan_copy_kernel(PlanSource src, AttnArgs a, int P_req, long long cap) {
+  pdl_trigger();
+  pdl_wait();
+  if (blockIdx.x == 0) {
+    make_plan(src, a.B, P_req, cap, a.plan_tile, a.ws, a.L, a.status);
+    return;
+  }
+  const int b = (blockIdx.x - 1) / kCopyBlocks, r0 = (blockIdx.x - 1) % kCopyBlocks * kCopyRows;
+  const long long cached = min(max((long long)src.ctx_len[b], 0ll), cap);
+  const long long end = min(cached + src.drafted, cap);
+  const long long first = cached / kTile * kTile;
+  if (first + r0 >= ceil_div_ll(end, kTile) * kTile) return;   // a block that is not there
+  uint4 *dst = reinterpret_cast<uint4 *>(a.ws + a.tree.copy_off) + ((long long)b * kTreeCopyRows + r0) * 72;
+  for (int u = threadIdx.x; u < kCopyRows * 72; u += blockDim.x) {
+    const long long t = first + r0 + u / 72;
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (t < end) {
+      const long long row = token_row(a, b, t);
+      if (row >= 0) v = reinterpret_cast<const uint4 *>(a.cache)[row * 72 + u % 72];
+      else atomicOr(a.status, kStatusBounds);
+      if (t >= cached) v = finite_or_zero(v);
+    }
+    dst[u] = v;
   }
 }
 
@@ -171,8 +245,10 @@ __device__ __forceinline__ int fp8_group_of(int f, int d_c) {
 }
 
 // T: element type of the query; F8: the cache holds E4M3 codes with group
-// scales (else elements of type T).
-template <typename T, bool F8>
+// scales (else elements of type T).  Tree: plan sequence b holds the heads of
+// one drafted token (b / T its batch sequence, b % T the token); a drafted
+// token that is masked is skipped, so whatever its row holds reaches nothing.
+template <typename T, bool F8, bool kTree>
 __global__ void __launch_bounds__(256) attn_simt_kernel(AttnArgs a) {
   const WsHeader *hd = reinterpret_cast<const WsHeader *>(a.ws);
   const long long P = hd->P, Ttot = hd->Ttot;
@@ -199,9 +275,12 @@ __global__ void __launch_bounds__(256) attn_simt_kernel(AttnArgs a) {
     if (s0 >= s1) continue;
     const long long piece = pb[b] + (w - plan_share_of_tile(tp[b], P, Ttot));
     const int ctx = plan_ctx(a.ws, a.L, b);
-    const long long beg = plan_begin_tok(a.ws, a.L, b, a.B);
+    const long long beg = plan_begin_tok(a, b);
     const long long p_begin = beg + (s0 - tp[b]) * a.plan_tile;
     const long long p_end = min((long long)ctx, beg + (s1 - tp[b]) * a.plan_tile);
+    const int seq = kTree ? b / a.tree.T : b;
+    const int cached = kTree ? plan_cached(a, b) : 0;
+    const unsigned long long bits = kTree ? a.tree.mask[b] : 0ull;
 
     float q[kQPerLane];
 #pragma unroll
@@ -215,7 +294,8 @@ __global__ void __launch_bounds__(256) attn_simt_kernel(AttnArgs a) {
     float m = -CUDART_INF_F, l = 0.f;
 
     for (long long p = p_begin; p < p_end; ++p) {
-      const long long row = cache_row(b, p, a.cache_len, a.block_table, a.max_blocks, a.page_size);
+      if (kTree && p >= cached && !((bits >> (p - cached)) & 1ull)) continue;
+      const long long row = a.sel ? selected_row(a, b, p, ctx) : token_row(a, seq, p);
       if (row < 0) {
         if (lane == 0) atomicOr(a.status, kStatusBounds);
         continue;
@@ -244,6 +324,26 @@ __global__ void __launch_bounds__(256) attn_simt_kernel(AttnArgs a) {
         if (f < a.d_c) o[j] = o[j] * corr + pr * val[j];
       }
       m = m_new;
+    }
+    if (kTree) {
+      // a row that attends nothing is zero; a NaN sum stays NaN
+      const TreePiece tpc = tree_piece(tp, b, w, P, Ttot);
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const float z = l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * 0.69314718055994531f;
+      const long long orow = (long long)b * a.n_h + h, prow = part_row(a.L, tpc.slot, h);
+      T *out = reinterpret_cast<T *>(a.tree.out) + orow * a.d_c;
+#pragma unroll
+      for (int j = 0; j < kOPerLane; ++j) {
+        const int f = lane + 32 * j;
+        if (f >= a.d_c) continue;
+        if (tpc.whole) out[f] = from_f<T>(o[j] * inv);
+        else opart[prow * a.d_c + f] = o[j] * inv;
+      }
+      if (lane == 0) {
+        if (!tpc.whole) lse[prow] = z;
+        else if (a.tree.lse) a.tree.lse[orow] = z;
+      }
+      continue;
     }
     const float inv = l > 0.f ? 1.f / l : 0.f;
     float *dst = opart + part_row(a.L, piece, h) * (long long)a.d_c;
@@ -297,7 +397,7 @@ template <typename T>
 __global__ void __launch_bounds__(256) append_simt_kernel(
     const T *h, int T_new, int d, int d_c, int d_r, const int *start_pos, const T *w_dkv,
     const T *w_kr, T *cache, long long cache_len, const int *block_table, int max_blocks,
-    int page_size, const double *theta, unsigned *status, float *rows_out) {
+    int page_size, const double *theta, unsigned *status, float *rows_out, const int *depth) {
   extern __shared__ float sh[];
   const long long tok = blockIdx.x;
   const int b = (int)(tok / T_new), t = (int)(tok % T_new);
@@ -319,8 +419,9 @@ __global__ void __launch_bounds__(256) append_simt_kernel(
   if (lane != 0) return;
   const long long p = (long long)start_pos[b] + t;
   if (f0 >= d_c) {
+    const long long rp = depth ? (long long)start_pos[b] + depth[tok] : p;   // the position it is rotated by
     double sn, cs;
-    sincos((double)p * theta[(f0 - d_c) >> 1], &sn, &cs);
+    sincos((double)rp * theta[(f0 - d_c) >> 1], &sn, &cs);
     const float c = (float)cs, s = (float)sn;
     const float r0 = a0 * c - a1 * s, r1 = a0 * s + a1 * c;
     a0 = r0;
@@ -522,13 +623,19 @@ __global__ void __launch_bounds__(256) linear_simt_kernel(const T *o, const T *w
 // ---------------------------------------------------------------------------
 // launchers
 // ---------------------------------------------------------------------------
-cudaError_t launch_plan(const int *ctx_begin, const int *ctx_len, int B, int P, long long cap, int tile, char *ws,
-                        const WsLayout &L, unsigned *status, cudaStream_t s) {
+cudaError_t launch_plan(const PlanSource &src, int B, int P, long long cap, int tile, char *ws, const WsLayout &L,
+                        unsigned *status, cudaStream_t s) {
   if (tile < kTile || tile % kTile != 0) return cudaErrorInvalidValue;
   // one thread per sequence up to 1024 (each thread takes a run of sequences beyond)
   const int threads = B >= 1024 ? 1024 : (B <= 32 ? 32 : (B + 31) / 32 * 32);
-  return launch_pdl(plan_kernel, dim3(1), dim3(threads), 0, s, 1, ctx_begin, ctx_len, B, P, cap, tile, ws, L,
-                    status);
+  return launch_pdl(plan_kernel, dim3(1), dim3(threads), 0, s, 1, src, B, P, cap, tile, ws, L, status);
+}
+
+cudaError_t launch_tree_plan_copy(const PlanSource &src, const AttnArgs &a, int P, long long cap, cudaStream_t s) {
+  const int batch = a.B / src.groups;
+  if (a.d_c + a.d_r != 576 || src.drafted > kTreeMaxDrafted) return cudaErrorNotSupported;
+  const int threads = a.B >= 1024 ? 1024 : (a.B <= 288 ? 288 : (a.B + 31) / 32 * 32);
+  return launch_pdl(tree_plan_copy_kernel, dim3(1 + batch * kCopyBlocks), dim3(threads), 0, s, 1, src, a, P, cap);
 }
 
 cudaError_t launch_attn_simt(const AttnArgs &a, int P, bool fp32, cudaStream_t s) {
@@ -536,10 +643,19 @@ cudaError_t launch_attn_simt(const AttnArgs &a, int P, bool fp32, cudaStream_t s
   const int warps = a.n_h < 8 ? a.n_h : 8;
   dim3 grid(P, (a.n_h + warps - 1) / warps);
   const bool f8 = a.kv_scale != nullptr;
-  if (fp32 && f8) attn_simt_kernel<float, true><<<grid, warps * 32, 0, s>>>(a);
-  else if (fp32) attn_simt_kernel<float, false><<<grid, warps * 32, 0, s>>>(a);
-  else if (f8) attn_simt_kernel<__nv_bfloat16, true><<<grid, warps * 32, 0, s>>>(a);
-  else attn_simt_kernel<__nv_bfloat16, false><<<grid, warps * 32, 0, s>>>(a);
+  if (fp32 && f8) attn_simt_kernel<float, true, false><<<grid, warps * 32, 0, s>>>(a);
+  else if (fp32) attn_simt_kernel<float, false, false><<<grid, warps * 32, 0, s>>>(a);
+  else if (f8) attn_simt_kernel<__nv_bfloat16, true, false><<<grid, warps * 32, 0, s>>>(a);
+  else attn_simt_kernel<__nv_bfloat16, false, false><<<grid, warps * 32, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_tree_attn_simt(const AttnArgs &a, int P, bool fp32, cudaStream_t s) {
+  if (a.d_c + a.d_r > kSimtMaxD || a.d_c > kSimtMaxC) return cudaErrorNotSupported;
+  const int warps = a.n_h < 8 ? a.n_h : 8;
+  dim3 grid(P, (a.n_h + warps - 1) / warps);
+  if (fp32) attn_simt_kernel<float, false, true><<<grid, warps * 32, 0, s>>>(a);
+  else attn_simt_kernel<__nv_bfloat16, false, true><<<grid, warps * 32, 0, s>>>(a);
   return cudaGetLastError();
 }
 
@@ -692,7 +808,7 @@ cudaError_t launch_append_simt(const mla_config &cfg, const void *h, int B, int 
                                const int *start_pos, const void *w_dkv, const void *w_kr,
                                void *cache, long long cache_len, const int *block_table,
                                int max_blocks, const double *theta, unsigned *status,
-                               cudaStream_t s, float *rows_out) {
+                               cudaStream_t s, float *rows_out, const int *depth) {
   const int D = cfg.d_c + cfg.d_r;
   dim3 grid((unsigned)((long long)B * T), (D / 2 + 7) / 8);
   const size_t smem = sizeof(float) * cfg.d_model;
@@ -701,12 +817,12 @@ cudaError_t launch_append_simt(const mla_config &cfg, const void *h, int B, int 
     append_simt_kernel<float><<<grid, 256, smem, s>>>(
         (const float *)h, T, cfg.d_model, cfg.d_c, cfg.d_r, start_pos, (const float *)w_dkv,
         (const float *)w_kr, (float *)cache, cache_len, block_table, max_blocks, cfg.page_size,
-        theta, status, rows_out);
+        theta, status, rows_out, depth);
   else
     append_simt_kernel<__nv_bfloat16><<<grid, 256, smem, s>>>(
         (const __nv_bfloat16 *)h, T, cfg.d_model, cfg.d_c, cfg.d_r, start_pos,
         (const __nv_bfloat16 *)w_dkv, (const __nv_bfloat16 *)w_kr, (__nv_bfloat16 *)cache,
-        cache_len, block_table, max_blocks, cfg.page_size, theta, status, rows_out);
+        cache_len, block_table, max_blocks, cfg.page_size, theta, status, rows_out, depth);
   return cudaGetLastError();
 }
 

@@ -37,6 +37,19 @@
 // warps 2-5 softmax, O rescale and epilogue (one thread per tensor-memory
 // lane).
 //
+// Tree of drafted tokens (kTree): the query rows of a sequence are (drafted
+// token, head), any number of them, cut into groups of 128; a group takes the
+// place of the 128 heads of one sequence and walks the cached tokens and the
+// drafted ones behind them.  Only tiles that reach past the cached tokens look
+// at the mask: a row's validity for its 128 columns is four 32-bit words built
+// from its 64-bit mask by shifts.  P.V takes the one or two blocks that hold
+// drafted tokens (and the zeros behind them) from a copy that the plan's
+// launch made, with non-finite values replaced by zero: a masked token has
+// probability 0, but 0 * NaN would reach every row of the tile (a row that
+// does attend such a token has a NaN score and so a NaN result).  That copy
+// also spares every group the copy by hand.  A group whose tiles lie in one
+// share is written out in bf16 at once, without a partial.
+//
 // Every wait is bounded; a wait that runs out flags MLA_ERR_TIMEOUT and the
 // kernel winds down without further waits.
 #include <math_constants.h>
@@ -102,11 +115,13 @@ constexpr uint32_t kIdescQK = idesc_bf16(128, kTileTok, false, false);
 constexpr uint32_t kIdescPV = idesc_bf16(128, 256, false, true);
 
 struct Piece {
-  int b;
+  int b;               // batch sequence
+  int v;               // plan sequence (b, or a row group of b for a tree)
   long long piece;     // global piece index
   int tok_begin;       // first token of the piece in sequence b
   int tok_end;         // one past the last token attended by this piece
   int ctx;             // the sequence's context length (clamped to the cache)
+  int cached;          // tokens before the drafted ones (ctx without a tree)
   int ntiles;          // 256-token MMA tiles
 };
 
@@ -135,6 +150,7 @@ __device__ __forceinline__ void walk_init(Walk &w, const AttnArgs &a, int share)
 }
 
 // Next piece of this share; false when done.
+template <bool kTree>
 __device__ __forceinline__ bool walk_next(Walk &w, const AttnArgs &a, int share, Piece &pc) {
   while (w.b < w.B && w.tp[w.b] < w.t1) {
     const int b = w.b++;
@@ -142,8 +158,10 @@ __device__ __forceinline__ bool walk_next(Walk &w, const AttnArgs &a, int share,
     const long long s1 = w.t1 < w.tp[b + 1] ? w.t1 : w.tp[b + 1];
     if (s0 >= s1) continue;
     const int ctx = plan_ctx(a.ws, a.L, b);
-    const int beg = plan_begin_tok(a.ws, a.L, b, a.B);
-    pc.b = b;
+    const int beg = kTree ? 0 : plan_begin_tok(a, b);
+    pc.b = kTree ? b / a.tree.groups : b;
+    pc.v = b;
+    pc.cached = kTree ? plan_cached(a, b) : ctx;
     pc.piece = w.pb[b] + (share - plan_share_of_tile(w.tp[b], w.P, w.Ttot));
     pc.tok_begin = beg + (int)((s0 - w.tp[b]) * a.plan_tile);
     const long long e = beg + (s1 - w.tp[b]) * a.plan_tile;
@@ -155,14 +173,22 @@ __device__ __forceinline__ bool walk_next(Walk &w, const AttnArgs &a, int share,
   return false;
 }
 
-// Cache row of token t of sequence b, or -1 (unmapped / outside the cache).
-__device__ __forceinline__ long long kv_row(const AttnArgs &a, int b, int t) {
-  if (a.page_size == 0) return (long long)b * a.cache_len + t;
-  const int bi = t / kTile;
-  if (bi >= a.max_blocks) return -1;
-  const int blk = a.block_table[(long long)b * a.max_blocks + bi];
-  if (blk < 0 || blk >= a.cache_len) return -1;
-  return (long long)blk * kTile + (t % kTile);
+// Cache row of token t of the piece's sequence, or -1 (unmapped / outside the cache).
+template <bool kTree>
+__device__ __forceinline__ long long kv_row(const AttnArgs &a, const Piece &p, int t) {
+  return !kTree && a.sel ? selected_row(a, p.b, t, p.ctx) : token_row(a, p.b, t);
+}
+
+// Bits of word w (columns 32w .. 32w + 31) of a row's validity: column c holds
+// token base + c, valid below `cached` and, past it, where `bits` has the
+// drafted token's bit; `n` columns lie inside the piece.
+__device__ __forceinline__ uint32_t tree_valid(int w, int base, int n, int cached, unsigned long long bits) {
+  auto below = [](int k) { return k <= 0 ? 0u : (k >= 32 ? 0xffffffffu : (1u << k) - 1u); };
+  const int sh = cached - base - 32 * w;     // column of the first drafted token within the word
+  uint32_t d = 0;
+  if (sh >= 0 && sh < 32) d = (uint32_t)(bits << sh);
+  else if (sh < 0 && sh > -64) d = (uint32_t)(bits >> -sh);
+  return (below(sh) | d) & below(n - 32 * w);
 }
 
 struct Bars {
@@ -195,9 +221,10 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, unsign
 // Row coordinate of a block of cache rows starting at token t0 of the piece's
 // sequence, or an out-of-range row (TMA then fills zeros) when the block
 // starts past the piece.
+template <bool kTree>
 __device__ __forceinline__ int block_row(const AttnArgs &a, const Piece &p, int t0, long long kv_rows) {
   if (t0 >= p.tok_end) return (int)kv_rows;
-  const long long r = kv_row(a, p.b, t0);
+  const long long r = kv_row<kTree>(a, p, t0);
   if (r < 0) {
     atomicOr(a.status, kStatusBounds);
     return (int)kv_rows;
@@ -212,10 +239,11 @@ __device__ __forceinline__ int tile_subs(const Piece &p, int t0) {
   return (n + kSubTok - 1) / kSubTok;
 }
 
+template <bool kTree>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     attn_pair_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
                      const __grid_constant__ CUtensorMap mapV, const __grid_constant__ CUtensorMap mapV2,
-                     const AttnArgs a, const long long kv_rows) {
+                     const __grid_constant__ CUtensorMap mapT, const AttnArgs a, const long long kv_rows) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t *sQ = sm + kOffQ;
@@ -276,6 +304,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // leader arms each slot with the bytes both CTAs' loads bring (the peer's
     // loads count on the leader's barrier directly).  Warp 0 also loads Q.
     const int pid = producer_index(warp);
+    const bool boxes64 = a.page_size != 0 || (!kTree && a.sel != nullptr);
     const uint32_t lq = ptx::leader_addr(bars.qfull());
     const uint32_t lf0 = ptx::leader_addr(bars.full(0));
     if (lane == 0) {
@@ -324,7 +353,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (s < 0) return false;
           uint8_t *dst = sRing + s * kSlot;
           const int tok0 = t0 + kSubTok * t;
-          if (tok0 + kSubTok > p.ctx) {
+          if (!kTree && tok0 + kSubTok > p.ctx) {
             // The block runs past the sequence: the leader copies the valid
             // rows of both CTAs' column halves by hand and zeroes the rest,
             // so that no unwritten cache row (possibly NaN) reaches P.V.
@@ -337,7 +366,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const int tk = tok0 + row;
                 uint4 v = make_uint4(0, 0, 0, 0);
                 if (tk < p.ctx) {
-                  const long long r = kv_row(a, p.b, tk);
+                  const long long r = kv_row<kTree>(a, p, tk);
                   if (r >= 0)
                     v = *reinterpret_cast<const uint4 *>(reinterpret_cast<const __nv_bfloat16 *>(a.cache) +
                                                          r * 576 + 256 * g + 128 * cta + 64 * half + 8 * c);
@@ -353,14 +382,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               if (lane == 0) ptx::mbar_arrive(bars.full(s));
             }
           } else if (lane == 0) {
-            const int y = block_row(a, p, tok0, kv_rows);
+            // a tree's last blocks come from their copy
+            const bool copied = kTree && tok0 + kSubTok > p.cached;
+            const int y = copied ? p.b * kTreeCopyRows + tok0 - p.cached / kTile * kTile
+                                 : block_row<kTree>(a, p, tok0, kv_rows);
+            const CUtensorMap *map = copied ? &mapT : &mapV2;
             if (leader) ptx::mbar_arrive_expect_tx(bars.full(s), 2 * kSlot);
             const int feat0 = 256 * g + 128 * (int)rank;
             // one 3D box: 64 rows x both 64-column chunks (chunk index feat0 / 64)
 #if MLA_PAIR_EVICT
-            ptx::tma_load_3d_pair_hint(dst, &mapV2, lf0 + 8 * s, 0, y, feat0 / 64, last_read);
+            ptx::tma_load_3d_pair_hint(dst, map, lf0 + 8 * s, 0, y, feat0 / 64, last_read);
 #else
-            ptx::tma_load_3d_pair(dst, &mapV2, lf0 + 8 * s, 0, y, feat0 / 64);
+            ptx::tma_load_3d_pair(dst, map, lf0 + 8 * s, 0, y, feat0 / 64);
 #endif
           }
           ++sc;
@@ -368,14 +401,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       return true;
     };
-    while (ok && walk_next(w, a, share, pc)) {
+    while (ok && walk_next<kTree>(w, a, share, pc)) {
       bool qok = true;
       if (lane == 0) {
         if (pid == 0 && npc > 0) qok = ptx::mbar_wait(bars.qempty(), (npc - 1) & 1, a.status, abort_flag);
         if (pid == 0 && qok) {
           if (leader) ptx::mbar_arrive_expect_tx(bars.qfull(), 2 * kQBytes);
-          for (int c = 0; c < 9; ++c)
-            ptx::tma_load_2d_pair(sQ + c * 8192, &mapQ, lq, 64 * c, pc.b * 128 + 64 * (int)rank);
+          for (int c = 0; c < 9; ++c) {
+            if (kTree)   // rows past the sequence's are zero-filled
+              ptx::tma_load_3d_pair(sQ + c * 8192, &mapQ, lq, 64 * c,
+                                    128 * (pc.v - pc.b * a.tree.groups) + 64 * (int)rank, pc.b);
+            else
+              ptx::tma_load_2d_pair(sQ + c * 8192, &mapQ, lq, 64 * c, pc.b * 128 + 64 * (int)rank);
+          }
         }
       }
       if (!__shfl_sync(0xffffffffu, qok ? 1 : 0, 0)) break;
@@ -385,8 +423,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int tr = t0 + kHalfTok * (int)rank;
         int y0 = 0, y1 = 0;
         if (lane == 0) {
-          y0 = block_row(a, pc, tr, kv_rows);
-          if (a.page_size) y1 = block_row(a, pc, tr + kSubTok, kv_rows);
+          y0 = block_row<kTree>(a, pc, tr, kv_rows);
+          if (boxes64) y1 = block_row<kTree>(a, pc, tr + kSubTok, kv_rows);
         }
         for (int c = 0; c < 9; ++c) {
           const int s = acquire();
@@ -395,10 +433,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (lane == 0) {
             uint8_t *dst = sRing + s * kSlot;
             if (leader) ptx::mbar_arrive_expect_tx(bars.full(s), 2 * kSlot);
-            if (a.page_size == 0) {
+            if (!boxes64) {
               ptx::tma_load_2d_pair(dst, &mapK, lf0 + 8 * s, 64 * c, y0);
             } else {
-              // 64-token pages: two 64-row boxes.
+              // 64-token pages or selected blocks: two 64-row boxes.
               ptx::tma_load_2d_pair(dst, &mapV, lf0 + 8 * s, 64 * c, y0);
               ptx::tma_load_2d_pair(dst + 8192, &mapV, lf0 + 8 * s, 64 * c, y1);
             }
@@ -473,7 +511,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ptx::mma_commit_pair_both(bars.odone(t.i & 1));
         return true;
       };
-      while (ok && walk_next(w, a, share, pc)) {
+      while (ok && walk_next<kTree>(w, a, share, pc)) {
         if (!ptx::mbar_wait(bars.qfull(), npc & 1, a.status, abort_flag)) { ok = false; break; }
         for (int k = 0; k < pc.ntiles && ok; ++k) {
           const uint32_t dS = tmem + (i & 1) * kColS;
@@ -519,8 +557,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     Piece pc;
     int i = 0, npc_s = 0;
     bool ok = true;
-    while (ok && walk_next(w, a, share, pc)) {
+    while (ok && walk_next<kTree>(w, a, share, pc)) {
       float m_run = -CUDART_INF_F, l_part = 0.f;
+      // tree: this thread's query row of the sequence, and its drafted tokens
+      const int row = 128 * (pc.v - pc.b * a.tree.groups) + 64 * (int)rank + h;
+      unsigned long long bits = 0ull;
+      if (kTree && row < a.tree.seq_rows) {
+        bits = a.tree.mask[(long long)pc.b * a.tree.T + row / a.n_h];
+        if (a.tree.T < 64) bits &= (1ull << a.tree.T) - 1ull;
+      }
       for (int k = 0; k < pc.ntiles; ++k, ++i) {
         const int base = pc.tok_begin + kTileTok * k + kHalfTok * th;
         const int nvalid = min(max(pc.tok_end - base, 0), kHalfTok);
@@ -532,10 +577,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ptx::tmem_ld64_sync(scol, reinterpret_cast<uint32_t *>(v));
         ptx::tmem_ld64_sync(scol + 64, reinterpret_cast<uint32_t *>(v) + 64);
         float mx[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+        if (kTree) {
+          uint32_t ok[4];
 #pragma unroll
-        for (int j = 0; j < kHalfTok; ++j) {
-          v[j] = j < nvalid ? v[j] * a.scale_log2 : -CUDART_INF_F;
-          mx[j & 3] = fmaxf(mx[j & 3], v[j]);
+          for (int w4 = 0; w4 < 4; ++w4)
+            ok[w4] = base + kHalfTok <= pc.cached ? 0xffffffffu : tree_valid(w4, base, nvalid, pc.cached, bits);
+#pragma unroll
+          for (int j = 0; j < kHalfTok; ++j) {
+            v[j] = (ok[j >> 5] >> (j & 31)) & 1u ? v[j] * a.scale_log2 : -CUDART_INF_F;
+            mx[j & 3] = fmaxf(mx[j & 3], v[j]);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < kHalfTok; ++j) {
+            v[j] = j < nvalid ? v[j] * a.scale_log2 : -CUDART_INF_F;
+            mx[j & 3] = fmaxf(mx[j & 3], v[j]);
+          }
         }
         const float mloc = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
         red_m[(i & 1) * 128 + l] = mloc;
@@ -553,11 +610,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         // Probabilities (bf16 pairs) and their sum, before waiting for the
         // previous tile's P.V, so that only the store below waits for it.
+        // A row with nothing valid so far (a tree's masks) subtracts 0: -inf - -inf is NaN.
+        const float m_use = kTree && m_run == -CUDART_INF_F ? 0.f : m_run;
         uint32_t pk[kHalfTok / 2];
         float ps[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int j = 0; j < kHalfTok / 2; ++j) {
-          const float p0 = ptx::exp2_approx(v[2 * j] - m_run), p1 = ptx::exp2_approx(v[2 * j + 1] - m_run);
+          const float p0 = ptx::exp2_approx(v[2 * j] - m_use), p1 = ptx::exp2_approx(v[2 * j + 1] - m_use);
           ps[j & 7] += p0 + p1;
           __nv_bfloat162 b2 = __floats2bfloat162_rn(p0, p1);
           pk[j] = *reinterpret_cast<uint32_t *>(&b2);
@@ -613,14 +672,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const float lsum = l_part + red_l[l ^ 64];
       if (!warp_wait(bars.odone((i - 1) & 1), ((i - 1) >> 1) & 1, a.status, abort_flag)) { ok = false; break; }
       ptx::tc_fence_after();
-      const float inv = lsum > 0.f ? 1.f / lsum : 0.f;
       const int head = 64 * (int)rank + h;
-      float *dst = opart + part_row(a.L, pc.piece, head) * (long long)a.d_c + 128 * th;
+      // a tree's row that attends nothing is zero, a NaN sum stays NaN
+      const float inv = (kTree ? lsum != 0.f : lsum > 0.f) ? 1.f / lsum : 0.f;
+      const float z = (kTree ? lsum != 0.f : lsum > 0.f) ? (m_run + log2f(lsum)) * 0.69314718055994531f : -CUDART_INF_F;
+      long long slot = pc.piece;
+      bool whole = false;
+      if (kTree) {
+        const TreePiece t = tree_piece(w.tp, pc.v, share, w.P, w.Ttot);
+        whole = t.whole;
+        slot = t.slot;
+      }
+      float *dst = opart + part_row(a.L, slot, head) * (long long)a.d_c + 128 * th;
+      const long long orow = (long long)pc.b * a.tree.seq_rows + row;
+      __nv_bfloat16 *out = reinterpret_cast<__nv_bfloat16 *>(a.tree.out) + orow * a.d_c + 128 * th;
 #pragma unroll 1
       for (int c = 0; c < 16; ++c) {
         uint32_t r[16];
         ptx::tmem_ld16(lane_addr + kColO + 16 * c, r);
         ptx::tmem_ld_wait();
+        if (kTree && whole) {
+          if (row < a.tree.seq_rows) {
+            uint32_t o[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const __nv_bfloat162 b2 =
+                  __floats2bfloat162_rn(__uint_as_float(r[2 * j]) * inv, __uint_as_float(r[2 * j + 1]) * inv);
+              o[j] = *reinterpret_cast<const uint32_t *>(&b2);
+            }
+            uint4 *d = reinterpret_cast<uint4 *>(out + (c >> 3) * 256 + (c & 7) * 16);
+            d[0] = make_uint4(o[0], o[1], o[2], o[3]);
+            d[1] = make_uint4(o[4], o[5], o[6], o[7]);
+          }
+          continue;
+        }
+        if (kTree && row >= a.tree.seq_rows) continue;
         float *d = dst + (c >> 3) * 256 + (c & 7) * 16;
 #pragma unroll
         for (int j = 0; j < 16; j += 4)
@@ -628,9 +714,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               make_float4(__uint_as_float(r[j]) * inv, __uint_as_float(r[j + 1]) * inv,
                           __uint_as_float(r[j + 2]) * inv, __uint_as_float(r[j + 3]) * inv);
       }
-      if (th == 0)
-        lse_out[part_row(a.L, pc.piece, head)] =
-            lsum > 0.f ? (m_run + log2f(lsum)) * 0.69314718055994531f : -CUDART_INF_F;
+      if (th == 0 && !(kTree && row >= a.tree.seq_rows)) {
+        if (!whole) lse_out[part_row(a.L, slot, head)] = z;
+        else if (a.tree.lse) a.tree.lse[orow] = z;
+      }
       ptx::tc_fence_before();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive_remote_addr(leader_ofree);
@@ -650,16 +737,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
 }  // namespace
 
-cudaError_t launch_attn_tc_pair(const AttnArgs &a, int P, cudaStream_t s) {
-  if (a.n_h != 128 || a.d_c != 512 || a.d_r != 64) return cudaErrorNotSupported;
+namespace {
+template <bool kTree>
+cudaError_t launch_pair(const AttnArgs &a, int P, cudaStream_t s, const std::function<cudaError_t()> *before) {
+  if (a.d_c != 512 || a.d_r != 64) return cudaErrorNotSupported;
   if (a.page_size != 0 && a.page_size != kTile) return cudaErrorNotSupported;
-  const long long rows = a.page_size ? a.cache_len * kTile : (long long)a.B * a.cache_len;
+  const int batch = kTree ? a.B / a.tree.groups : a.B;
+  const long long rows = a.page_size ? a.cache_len * kTile : (long long)batch * a.cache_len;
   if (rows <= 0 || rows >= (1ll << 31) - 256) return cudaErrorNotSupported;
-  CUtensorMap mq, mk, mv, mv2;
-  const uint64_t dq[2] = {576, (uint64_t)a.B * 128};
+  CUtensorMap mq, mk, mv, mv2, mt;
+  // queries: [B * 128 rows], or [B][seq_rows] for a tree, 64 rows to a box
+  const uint64_t dq[3] = {576, kTree ? (uint64_t)a.tree.seq_rows : (uint64_t)a.B * 128, (uint64_t)batch};
+  const uint64_t sq[2] = {576 * 2, 576 * 2 * dq[1]};
   const uint64_t dkv[2] = {576, (uint64_t)rows};
   const uint64_t st[1] = {576 * 2};
-  const uint32_t boxq[2] = {64, 64};
+  const uint32_t boxq[3] = {64, 64, 1};
   const uint32_t boxk[2] = {64, kHalfTok};
   const uint32_t boxv[2] = {64, kSubTok};
   // The cache viewed as [9 chunks][rows][64 columns]: one box of 64 rows x 2
@@ -667,17 +759,34 @@ cudaError_t launch_attn_tc_pair(const AttnArgs &a, int P, cudaStream_t s) {
   const uint64_t dkv3[3] = {64, (uint64_t)rows, 9};
   const uint64_t st3[2] = {576 * 2, 64 * 2};
   const uint32_t boxv3[3] = {64, kSubTok, 2};
-  if (!encode_map_bf16(&mq, a.q_abs, 2, dq, st, boxq, CU_TENSOR_MAP_SWIZZLE_128B) ||
+  if (!encode_map_bf16(&mq, a.q_abs, kTree ? 3 : 2, dq, sq, boxq, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !encode_map_bf16(&mk, a.cache, 2, dkv, st, boxk, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !encode_map_bf16(&mv, a.cache, 2, dkv, st, boxv, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !encode_map_bf16(&mv2, a.cache, 3, dkv3, st3, boxv3, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorNotSupported;
+  mt = mv2;
+  const uint64_t dt3[3] = {64, (uint64_t)batch * kTreeCopyRows, 9};
+  if (kTree && !encode_map_bf16(&mt, a.ws + a.tree.copy_off, 3, dt3, st3, boxv3, CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorNotSupported;
   static std::atomic<int> configured[kMaxDevices];
   cudaError_t e = once_per_device(configured, [] {
-    return cudaFuncSetAttribute(attn_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemAlloc);
+    return cudaFuncSetAttribute(attn_pair_kernel<kTree>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemAlloc);
   });
+  if (e == cudaSuccess && before) e = (*before)();
   if (e != cudaSuccess) return e;
-  return launch_pdl(attn_pair_kernel, dim3(2 * P), dim3(kThreads), kSmemAlloc, s, 1, mq, mk, mv, mv2, a, rows);
+  return launch_pdl(attn_pair_kernel<kTree>, dim3(2 * P), dim3(kThreads), kSmemAlloc, s, 1, mq, mk, mv, mv2, mt, a,
+                    rows);
+}
+}  // namespace
+
+cudaError_t launch_attn_tc_pair(const AttnArgs &a, int P, cudaStream_t s) {
+  if (a.n_h != 128) return cudaErrorNotSupported;
+  return launch_pair<false>(a, P, s, nullptr);
+}
+
+cudaError_t launch_tree_attn_tc_pair(const AttnArgs &a, int P, cudaStream_t s,
+                                     const std::function<cudaError_t()> &plan) {
+  return launch_pair<true>(a, P, s, &plan);
 }
 
 }  // namespace mla

@@ -162,7 +162,7 @@ __device__ __forceinline__ bool walk_next(Walk &w, const AttnArgs &a, int share,
     const long long s1 = w.t1 < w.tp[b + 1] ? w.t1 : w.tp[b + 1];
     if (s0 >= s1) continue;
     const int ctx = plan_ctx(a.ws, a.L, b);
-    const int beg = plan_begin_tok(a.ws, a.L, b, a.B);
+    const int beg = plan_begin_tok(a, b);
     pc.b = b;
     pc.piece = w.pb[b] + (share - plan_share_of_tile(w.tp[b], w.P, w.Ttot));
     pc.tok_begin = beg + (int)((s0 - w.tp[b]) * a.plan_tile);
@@ -175,13 +175,8 @@ __device__ __forceinline__ bool walk_next(Walk &w, const AttnArgs &a, int share,
   return false;
 }
 
-__device__ __forceinline__ long long kv_row(const AttnArgs &a, int b, int t) {
-  if (a.page_size == 0) return (long long)b * a.cache_len + t;
-  const int bi = t / kTile;
-  if (bi >= a.max_blocks) return -1;
-  const int blk = a.block_table[(long long)b * a.max_blocks + bi];
-  if (blk < 0 || blk >= a.cache_len) return -1;
-  return (long long)blk * kTile + (t % kTile);
+__device__ __forceinline__ long long kv_row(const AttnArgs &a, const Piece &p, int t) {
+  return a.sel ? selected_row(a, p.b, t, p.ctx) : token_row(a, p.b, t);
 }
 
 // Row coordinate of the 64-row block of cache rows starting at token t0 of the
@@ -189,7 +184,7 @@ __device__ __forceinline__ long long kv_row(const AttnArgs &a, int b, int t) {
 // block starts at or past the piece's end.
 __device__ __forceinline__ int block_row(const AttnArgs &a, const Piece &p, int t0, long long kv_rows) {
   if (t0 >= p.tok_end) return (int)kv_rows;
-  const long long r = kv_row(a, p.b, t0);
+  const long long r = kv_row(a, p, t0);
   if (r < 0) {
     atomicOr(a.status, kStatusBounds);
     return (int)kv_rows;
@@ -231,7 +226,7 @@ __device__ __forceinline__ void hand_copy_half(const AttnArgs &a, const Piece &p
   const int lane = threadIdx.x & 31;
   constexpr int kUnits = F8 ? 4 : 8;          // 16-byte units per row
   constexpr int kPer = 64 * kUnits / 32;      // units per lane
-  const long long r0 = kv_row(a, p.b, t0);
+  const long long r0 = kv_row(a, p, t0);
   if (r0 < 0 && lane == 0) atomicOr(a.status, kStatusBounds);
   uint4 v[kPer];
 #pragma unroll
@@ -366,7 +361,7 @@ __global__ void __launch_bounds__(Cfg<H, F8>::kThreads, 1)
           if (kind[h2] == 0 && lane == 0) y = block_row(a, pc, t, kv_rows);
           yy[h2] = __shfl_sync(0xffffffffu, y, 0);
         }
-        const bool whole = a.page_size == 0 && kind[0] == 0 && kind[1] == 0 && yy[0] < kv_rows &&
+        const bool whole = a.page_size == 0 && !a.sel && kind[0] == 0 && kind[1] == 0 && yy[0] < kv_rows &&
                            yy[1] == yy[0] + 64;
         const bool partial = kind[0] == 2 || kind[1] == 2;
         // One chunk (column block c) into `dst` as two 64-row halves `half`
@@ -766,7 +761,7 @@ __global__ void __launch_bounds__(Cfg<H, F8>::kThreads, 1)
 #pragma unroll
         for (int rr = 0; rr < NRR; ++rr) {
           const int t = tok0 + r0 + RS * rr;
-          const long long r = has(rr) && t < pc.ctx ? kv_row(a, pc.b, t) : -1;
+          const long long r = has(rr) && t < pc.ctx ? kv_row(a, pc, t) : -1;
 #pragma unroll
           for (int g = 0; g < kGroups8; ++g) sig[rr][g] = r >= 0 ? a.kv_scale[r * kGroups8 + g] : 0.f;
         }

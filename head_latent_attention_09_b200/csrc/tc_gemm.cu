@@ -114,6 +114,7 @@ struct GemmParams {
   // append: destination rows
   int T;
   const int *start_pos;
+  const int *depth;   // [B, T] or NULL: token n is rotated by start_pos + depth[n] instead of by its slot
   long long cache_len;
   const int *block_table;
   int max_blocks;
@@ -297,6 +298,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             row = dest_row(b, p, g);
             if (row < 0) atomicOr(g.status, kStatusBounds);
           }
+          if (g.depth) p = g.start_pos[b] + g.depth[n];
         }
         s_row[j] = row;
         s_pos[j] = p;
@@ -750,7 +752,7 @@ cudaError_t launch_wo_tc(const mla_config &c, const void *o, const void *w_o, vo
 cudaError_t launch_append_tc(const mla_config &c, const void *h, int B, int T, const int *start_pos,
                              const void *w_dkv, const void *w_kr, void *cache, long long cache_len,
                              const int *block_table, int max_blocks, const double *theta,
-                             unsigned *status, cudaStream_t s, float *rows_out) {
+                             unsigned *status, cudaStream_t s, float *rows_out, const int *depth) {
   if (!aligned16(h) || !aligned16(w_dkv) || !aligned16(w_kr)) return cudaErrorNotSupported;
   const long long N = (long long)B * T;
   if (N > 65535LL * 256) return cudaErrorNotSupported;
@@ -767,6 +769,7 @@ cudaError_t launch_append_tc(const mla_config &c, const void *h, int B, int T, c
   g.d_r = c.d_r;
   g.T = T;
   g.start_pos = start_pos;
+  g.depth = depth;
   g.cache_len = cache_len;
   g.block_table = block_table;
   g.max_blocks = max_blocks;

@@ -1,0 +1,168 @@
+// Tree of drafted tokens (speculative decoding): the merge of tree attention's
+// split groups, and the cache's side of accepting a path.
+#include <math_constants.h>
+
+#include "internal.cuh"
+
+namespace mla {
+namespace {
+
+template <typename T> __device__ __forceinline__ T cast(float x);
+template <> __device__ __forceinline__ float cast<float>(float x) { return x; }
+template <> __device__ __forceinline__ __nv_bfloat16 cast<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+
+// Log-sum-exp merge of the groups that are split between shares.  A share
+// boundary cuts at most one group, so block x takes the group that begins in
+// share x and runs on into share x + 1 (if there is one); y counts blocks of 8
+// query rows, one warp each.  Groups that lie in one share were written by the
+// attention kernel, so the traffic is that of at most 2 P pieces however many
+// groups there are.
+template <typename T>
+__global__ void __launch_bounds__(256) tree_combine_kernel(AttnArgs a) {
+  pdl_trigger();
+  pdl_wait();
+  const WsHeader *hd = reinterpret_cast<const WsHeader *>(a.ws);
+  const long long P = hd->P, Ttot = hd->Ttot;
+  const long long *tp = reinterpret_cast<const long long *>(a.ws + a.L.tile_prefix_off);
+  const float *lse = reinterpret_cast<const float *>(a.ws + a.L.lse_off);
+  const float *op = reinterpret_cast<const float *>(a.ws + a.L.opart_off);
+  T *out = reinterpret_cast<T *>(a.tree.out);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (Ttot == 0) {   // a cache without room for a single token: no row attends anything
+    const long long rows = (long long)(a.B / a.tree.groups) * a.tree.seq_rows;
+    const long long n = (long long)gridDim.x * gridDim.y * 8;
+    for (long long r = ((long long)blockIdx.y * gridDim.x + blockIdx.x) * 8 + warp; r < rows; r += n) {
+      for (int f = lane; f < a.d_c; f += 32) out[r * a.d_c + f] = cast<T>(0.f);
+      if (a.tree.lse && lane == 0) a.tree.lse[r] = -CUDART_INF_F;
+    }
+    return;
+  }
+  const long long w0 = blockIdx.x;
+  if (w0 + 1 >= P) return;
+  // the group that holds the first tile of the next share
+  const int v = reinterpret_cast<const int *>(a.ws + a.L.share_first_off)[w0 + 1];
+  const long long s0 = tp[v], s1 = tp[v + 1];
+  if (s0 >= plan_begin(w0 + 1, P, Ttot) || s0 < plan_begin(w0, P, Ttot)) return;   // begins elsewhere
+  const int r = blockIdx.y * 8 + warp;
+  const int b = v / a.tree.groups, row = (v - b * a.tree.groups) * a.tree.group_rows + r;
+  if (r >= a.tree.group_rows || row >= a.tree.seq_rows) return;
+  const long long w1 = plan_share_of_tile(s1 - 1, P, Ttot);
+  // partials: the last piece of share w0 (or its only one), the first of the others
+  auto part = [&](long long w) { return part_row(a.L, 2 * w + (s0 > plan_begin(w, P, Ttot) ? 1 : 0), r); };
+  float m = -CUDART_INF_F;
+  for (long long w = w0 + lane; w <= w1; w += 32) m = fmaxf(m, lse[part(w)]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  // A row that attends nothing has -inf everywhere (weights of 0 and no sum);
+  // a NaN keeps its way into the sum.
+  const float m_use = m == -CUDART_INF_F ? 0.f : m;
+  float tot = 0.f;
+  for (long long w = w0 + lane; w <= w1; w += 32) tot += expf(lse[part(w)] - m_use);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
+  const float inv = tot == 0.f ? 0.f : 1.f / tot;
+  const long long orow = (long long)b * a.tree.seq_rows + row;
+  for (int f0 = 0; f0 < a.d_c; f0 += 512) {
+    float acc[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) acc[i] = 0.f;
+#pragma unroll 2
+    for (long long w = w0; w <= w1; ++w) {
+      const long long pr = part(w);
+      const float wt = expf(lse[pr] - m_use) * inv;
+      const float *src = op + pr * a.d_c + f0;
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (f0 + lane + 32 * i < a.d_c) acc[i] += wt * src[lane + 32 * i];
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (f0 + lane + 32 * i < a.d_c) out[orow * a.d_c + f0 + lane + 32 * i] = cast<T>(acc[i]);
+  }
+  if (a.tree.lse && lane == 0) a.tree.lse[orow] = tot == 0.f ? -CUDART_INF_F : m_use + logf(tot);
+}
+
+// Accepted path: row cached + path[i] -> cached + i, one block per sequence.
+// A path rises, so path[i] >= i and no store covers a row that is still to be
+// read when each column of the rows goes in path order: a thread carries
+// columns (units of up to 16 bytes), and issues the loads of kAhead rows
+// before their stores (a store to slot i lies below every source after i).
+// The traffic is at most 2 x 64 rows, so the time is that of the launch and
+// of two dependent reads.
+constexpr int kAhead = 8;
+template <typename U>
+__global__ void __launch_bounds__(1024) tree_accept_kernel(U *cache, int units, AttnArgs a, const int *ctx_len,
+                                                           const int *path, const int *n_path, int T, int *new_len) {
+  pdl_trigger();
+  pdl_wait();
+  const int b = blockIdx.x;
+  const long long cached = ctx_len[b];
+  const long long cap = a.page_size ? (long long)a.max_blocks * a.page_size : a.cache_len;
+  int n = n_path[b];
+  bool bad = n < 0 || n > T || cached < 0 || cached > cap;
+  if (bad) n = 0;
+  __shared__ long long src[kTreeMaxDrafted], dst[kTreeMaxDrafted];
+  for (int i = threadIdx.x; i < n; i += blockDim.x) {
+    const int p = path[(long long)b * T + i], q = i > 0 ? path[(long long)b * T + i - 1] : -1;
+    src[i] = p > q && p < T ? token_row(a, b, cached + p) : -1;
+    dst[i] = token_row(a, b, cached + i);
+    if (src[i] < 0 || dst[i] < 0) bad = true;
+  }
+  // With one wrong entry the whole sequence stays as it is.
+  bad = __syncthreads_or(bad);
+  if (bad) n = 0;
+  if (threadIdx.x == 0) {
+    if (bad) atomicOr(a.status, kStatusBounds);
+    if (new_len) new_len[b] = (int)cached + n;   // may be ctx_len itself: every thread has read it
+  }
+  for (int u = threadIdx.x; u < units; u += blockDim.x) {
+    for (int i0 = 0; i0 < n; i0 += kAhead) {
+      U v[kAhead];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k)
+        if (i0 + k < n) v[k] = cache[src[i0 + k] * units + u];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k)
+        if (i0 + k < n && src[i0 + k] != dst[i0 + k]) cache[dst[i0 + k] * units + u] = v[k];
+    }
+  }
+}
+
+template <typename U>
+cudaError_t accept_units(int row_bytes, void *cache, const AttnArgs &a, const int *ctx_len, const int *path,
+                         const int *n_path, int B, int T, int *new_len, cudaStream_t s) {
+  const int units = row_bytes / (int)sizeof(U);
+  const int threads = units >= 1024 ? 1024 : (units + 31) / 32 * 32;   // bf16 rows of 576: 72 units of 16 bytes
+  return launch_pdl(tree_accept_kernel<U>, dim3(B), dim3(threads), 0, s, 1, (U *)cache, units, a, ctx_len, path,
+                    n_path, T, new_len);
+}
+
+}  // namespace
+
+cudaError_t launch_tree_combine(const AttnArgs &a, int P, bool fp32, cudaStream_t s) {
+  const dim3 grid(P, (a.tree.group_rows + 7) / 8);
+  if (grid.y > 65535) return cudaErrorNotSupported;
+  return fp32 ? launch_pdl(tree_combine_kernel<float>, grid, dim3(256), 0, s, 1, a)
+              : launch_pdl(tree_combine_kernel<__nv_bfloat16>, grid, dim3(256), 0, s, 1, a);
+}
+
+cudaError_t launch_tree_accept(const mla_config &cfg, void *cache, long long cache_len, const int *block_table,
+                               int max_blocks, const int *ctx_len, const int *path, const int *n_path, int B, int T,
+                               int *new_len, unsigned *status, cudaStream_t s) {
+  AttnArgs a = {};
+  a.cache_len = cache_len;
+  a.block_table = block_table;
+  a.max_blocks = max_blocks;
+  a.page_size = cfg.page_size;
+  a.status = status;
+  const int row_bytes = (cfg.d_c + cfg.d_r) * (cfg.dtype == MLA_FP32 ? 4 : 2);
+  const uintptr_t mix = (uintptr_t)cache | (uintptr_t)row_bytes;
+  auto go = [&](auto unit) {
+    return accept_units<decltype(unit)>(row_bytes, cache, a, ctx_len, path, n_path, B, T, new_len, s);
+  };
+  if (mix % 16 == 0) return go(uint4{});
+  if (mix % 4 == 0) return go(uint32_t{});
+  return go(uint16_t{});
+}
+
+}  // namespace mla

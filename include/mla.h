@@ -412,6 +412,156 @@ int mla_decode_attn_fp8(mla_handle *handle, const void *q_abs, const void *cache
                         const int *ctx_len, int B, int num_parts, void *workspace, size_t ws_bytes,
                         mla_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * A tree of drafted tokens behind each sequence (speculative decoding: a draft
+ * proposes T tokens that continue a sequence along several branches, one pass
+ * of the model verifies them all, and the longest accepted branch is kept).
+ * V3's multi-token prediction drafts for this purpose (the "DeepSeek-V3"
+ * note's MTP section); the formulas are those of o_{t,i} with the sum over a
+ * token's own branch instead of over every earlier position.
+ *
+ * Drafted token t (0 <= t < T <= 64) of sequence b sits in cache slot
+ * ctx_len[b] + t, whatever its branch, and is rotated by the position it would
+ * have if its branch were kept, ctx_len[b] + depth[b, t] (depth 0: a direct
+ * continuation).  One step is
+ *   mla_cache_append_tree   the drafted rows
+ *   mla_absorb_q            with B * T queries and pos = ctx_len + depth
+ *   mla_tree_attn           ctx_lat of every drafted token
+ *   mla_out_proj            with B * T rows
+ * and, once the accepted branch is known,
+ *   mla_tree_accept         its rows move together behind the sequence.
+ * ------------------------------------------------------------------------- */
+
+/* mla_cache_append with separate slots and rotary positions: token t of
+ * sequence b is written at position ctx_len[b] + t and rotated by
+ * ctx_len[b] + depth[b, t].
+ *   depth  device int32 [B, T]
+ * T at most 64; other arguments and errors as for mla_cache_append. */
+int mla_cache_append_tree(mla_handle *handle, const void *h, int B, int T, const int *ctx_len, const int *depth,
+                          const void *w_dkv, const void *w_kr, void *cache, long long cache_len,
+                          const int *block_table, int max_blocks_per_seq, mla_stream_t stream);
+
+/* Bytes of workspace mla_tree_attn needs (num_parts 0: the default), into
+ * *bytes.  Host only.  Errors: INVALID_ARG (NULL, negative values, T > 64),
+ * UNSUPPORTED (too many rows for one call). */
+int mla_tree_workspace_size(const mla_handle *handle, int B, int T, int num_parts, size_t *bytes);
+
+/* Attention of the drafted tokens: token t of sequence b attends the ctx_len[b]
+ * cached tokens and those drafted tokens j (itself normally among them) whose
+ * bit j is set in tree_mask[b, t].
+ *   q_abs     [B, T, n_h, d_c+d_r]
+ *   ctx_len   device int32 [B], the tokens before the drafted ones.  A length
+ *             that the cache cannot hold is flagged and clamped as in
+ *             mla_decode_attn; so are drafted slots past the cache's end,
+ *             which are then attended by no token.
+ *   tree_mask device uint64 [B, T]; bits from T on are ignored.  A padding
+ *             token may have mask 0: it attends the cached tokens only.
+ *   ctx_lat   [B, T, n_h, d_c] (cfg.dtype), lse [B, T, n_h] float32 or NULL
+ *             (a row that attends nothing is zero with lse -inf)
+ *   workspace >= mla_tree_workspace_size(handle, B, T, num_parts) bytes, 256-byte
+ *             aligned, overwritten; no other call may use it at the same time.
+ * What a drafted row holds reaches only the tokens that attend it, NaN and
+ * infinities included (an infinity of the latent part that only ever meets a
+ * score of -inf counts as zero).  Results are deterministic for a fixed
+ * num_parts, and final: no mla_combine_splits follows.
+ * bf16 at d_c = 512, d_r = 64 (contiguous or 64-token pages) runs on the
+ * tensor cores for any n_h; other shapes and fp32 on the CUDA cores.
+ * Errors: INVALID_ARG, WORKSPACE, UNSUPPORTED (strict mode; more than 2^24
+ * groups of 128 query rows), CUDA. */
+int mla_tree_attn(mla_handle *handle, const void *q_abs, const void *cache, long long cache_len,
+                  const int *block_table, int max_blocks_per_seq, const int *ctx_len,
+                  const unsigned long long *tree_mask, int B, int T, int num_parts, void *ctx_lat, float *lse,
+                  void *workspace, size_t ws_bytes, mla_stream_t stream);
+
+/* Keeps the accepted branch: the cached row of drafted token path[b, i] moves
+ * from slot ctx_len[b] + path[b, i] to slot ctx_len[b] + i, for i < n_path[b];
+ * it was rotated for that position.  Slots behind the path keep what they hold.
+ *   path    device int32 [B, T], rising along the branch (the entries from
+ *           n_path[b] on are not read), n_path device int32 [B], 0 .. T
+ *   new_len device int32 [B] or NULL: receives ctx_len[b] + n_path[b]; may be
+ *           ctx_len itself
+ * A sequence with an entry that does not rise, lies outside 0 .. T-1 or outside
+ * the cache, or with n_path outside 0 .. T, stays as it is (new_len = ctx_len)
+ * and sets MLA_ERR_DEVICE_BOUNDS in the status word.  T at most 64.
+ * Errors: INVALID_ARG, CUDA. */
+int mla_tree_accept(mla_handle *handle, void *cache, long long cache_len, const int *block_table,
+                    int max_blocks_per_seq, const int *ctx_len, const int *path, const int *n_path, int B, int T,
+                    int *new_len, mla_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Sparse decode attention over selected blocks (long contexts).  A block is 64
+ * consecutive tokens of a sequence; block j holds tokens 64 j .. 64 j + 63, and
+ * n_j of them are cached.  All heads of absorbed attention read the same rows,
+ * so one selection per sequence serves them all.  One step is
+ *   mla_block_keys          mean rows of the blocks that hold new tokens
+ *   mla_block_scores        a score per block from the absorbed queries
+ *   mla_block_select        the k best blocks
+ *   mla_decode_attn_sparse  attention over them, then mla_combine_splits
+ * ------------------------------------------------------------------------- */
+
+/* Mean rows of blocks: keys[b, j] = (1 / n_j) sum of the block's cached rows
+ * [c^KV | k^R], summed in float32 and rounded once to cfg.dtype, for every
+ * block that holds a token of ctx_begin[b] .. ctx_len[b]-1 (the others keep
+ * their value).
+ *   ctx_begin  device int32 [B] or NULL (0: every block)
+ *   ctx_len    device int32 [B], the cached tokens after this step's append
+ *   max_new    host upper bound on ctx_len[b] - ctx_begin[b]; it sizes the
+ *              launch only, a longer range is still summarised whole
+ *   keys       [B, key_blocks, d_c+d_r] (cfg.dtype)
+ * Lengths the cache cannot hold are clamped, blocks beyond key_blocks and
+ * unmapped pages skipped, all flagged MLA_ERR_DEVICE_BOUNDS.
+ * Errors: INVALID_ARG, UNSUPPORTED (B above 65535), CUDA. */
+int mla_block_keys(mla_handle *handle, const void *cache, long long cache_len, const int *block_table,
+                   int max_blocks_per_seq, const int *ctx_begin, const int *ctx_len, int B, int max_new, void *keys,
+                   int key_blocks, mla_stream_t stream);
+
+/* Bytes of workspace mla_block_scores needs, into *bytes.  Host only.
+ * Errors: INVALID_ARG. */
+int mla_block_scores_workspace_size(const mla_handle *handle, int B, int key_blocks, size_t *bytes);
+
+/* Scores of the blocks of ctx_len[b] cached tokens:
+ *   x_ij = q_abs[b,i] . keys[b,j] / sqrt(d_h + d_r) + log n_j
+ *   scores[b,j] = sum over heads i of softmax_j(x_i)_j
+ * (the share of each head's attention that block j would draw if its tokens
+ * had the block's mean row; a sequence's scores add up to n_h).  Blocks beyond
+ * the sequence's get 0.  The scores are scaled as in mla_decode_attn
+ * (mla_set_rope_scaling included).
+ *   q_abs [B, n_h, d_c+d_r], keys [B, key_blocks, d_c+d_r], scores float32 [B, key_blocks]
+ * A sequence with more than key_blocks blocks is scored over the first
+ * key_blocks and flagged MLA_ERR_DEVICE_BOUNDS.  bf16 rows of d_c = 512, d_r = 64
+ * run on the tensor cores.  Errors: INVALID_ARG, WORKSPACE, UNSUPPORTED, CUDA. */
+int mla_block_scores(mla_handle *handle, const void *q_abs, const void *keys, int key_blocks, const int *ctx_len,
+                     int B, float *scores, void *workspace, size_t ws_bytes, mla_stream_t stream);
+
+/* The min(k, blocks) blocks of a sequence with the highest scores, in rising
+ * order: sel[b, 0 .. n_sel[b]-1], the rest of the row -1.  The first n_first
+ * and the last n_last blocks of the sequence rank above all others (whatever
+ * their scores, by the lower index if there are more than k); equal scores
+ * rank by the lower index, NaN below everything.
+ *   scores float32 [B, key_blocks], ctx_len device int32 [B] (blocks =
+ *   ceil(ctx_len / 64), at most key_blocks, more is flagged), sel device int32
+ *   [B, k], n_sel device int32 [B].
+ * Errors: INVALID_ARG (k above 2^20), UNSUPPORTED (more than 49152 blocks), CUDA. */
+int mla_block_select(mla_handle *handle, const float *scores, int key_blocks, const int *ctx_len, int B, int k,
+                     int n_first, int n_last, int *sel, int *n_sel, mla_stream_t stream);
+
+/* mla_decode_attn over the tokens of selected blocks only: blocks
+ * sel[b, 0 .. n_sel[b]-1] of sequence b (same workspace, same partials, merged
+ * by mla_combine_splits, mla_combine_splits_f32 or mla_combine_out_proj).
+ *   ctx_len device int32 [B] cached tokens, sel device int32 [B, k], n_sel
+ *   device int32 [B].  The blocks may come in any order, except that the
+ *   sequence's partial last block, if selected, comes last; a block listed
+ *   twice counts twice.  n_sel[b] = 0 gives a zero row with lse = -inf.
+ * A block the sequence does not have (or the partial one elsewhere) is flagged
+ * MLA_ERR_DEVICE_BOUNDS and not read, and that sequence's result is undefined;
+ * n_sel outside 0 .. min(k, blocks) is flagged and clamped.
+ * Errors as mla_decode_attn; INVALID_ARG for NULL sel or n_sel or k <= 0,
+ * UNSUPPORTED for pages that are not a multiple of 64 tokens. */
+int mla_decode_attn_sparse(mla_handle *handle, const void *q_abs, const void *cache, long long cache_len,
+                           const int *block_table, int max_blocks_per_seq, const int *ctx_len, const int *sel,
+                           const int *n_sel, int k, int B, int num_parts, void *workspace, size_t ws_bytes,
+                           mla_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -403,6 +403,91 @@ def combine_partials(parts):
 
 
 # ----------------------------------------------------------------------------
+# a tree of drafted tokens behind a sequence
+# ----------------------------------------------------------------------------
+
+def tree_bits(parents):
+    """Attention masks of drafted tokens from their parents (-1: the last cached
+    token): bit j of word t is set for t itself and every ancestor j."""
+    bits = []
+    for t, p in enumerate(parents):
+        bits.append((bits[p] if p >= 0 else 0) | 1 << t)
+    return bits
+
+
+def tree_depths(parents):
+    """Number of drafted ancestors of each drafted token: its rotary position
+    is the sequence's length plus this."""
+    depth = []
+    for p in parents:
+        depth.append(depth[p] + 1 if p >= 0 else 0)
+    return depth
+
+
+def tree_attention(q_abs, cached_rows, drafted_rows, bits, *, d_c: int, scale: float):
+    """Absorbed attention of T drafted tokens: token t attends the cached rows
+    and the drafted rows j with bit j of bits[t] set.  q_abs [T, h, D] ->
+    (ctx_lat [T, h, d_c], lse [T, h]); nothing attended gives 0 and -inf."""
+    T = len(bits)
+    out = []
+    for t in range(T):
+        mine = [j for j in range(T) if bits[t] >> j & 1]
+        rows = np.concatenate([np.asarray(cached_rows, F64), np.asarray(drafted_rows, F64)[mine]])
+        out.append(latent_attention(q_abs[t], rows, d_c=d_c, scale=scale))
+    return np.stack([o[0] for o in out]), np.stack([o[1] for o in out])
+
+
+def tree_accept(rows, cached: int, path):
+    """Cache rows of one sequence after keeping the drafted tokens of a path:
+    slot cached + i holds what slot cached + path[i] held."""
+    rows = np.array(rows)
+    rows[cached:cached + len(path)] = rows[[cached + p for p in path]]
+    return rows
+
+
+# ----------------------------------------------------------------------------
+# selection of blocks of cached tokens
+# ----------------------------------------------------------------------------
+
+BLOCK_TOKENS = 64
+
+
+def block_ranges(n: int):
+    return [(a, min(a + BLOCK_TOKENS, n)) for a in range(0, n, BLOCK_TOKENS)]
+
+
+def block_means(rows):
+    """Mean row of each block of a sequence's cached rows [n, D]."""
+    rows = np.asarray(rows, F64)
+    return np.array([rows[a:b].mean(axis=0) for a, b in block_ranges(len(rows))]).reshape(-1, rows.shape[1])
+
+
+def block_scores(q_abs, means, n: int, *, scale: float):
+    """Per block, the sum over heads of the softmax share the block would draw
+    if each of its tokens had the block's mean row (n cached tokens)."""
+    sizes = np.array([b - a for a, b in block_ranges(n)], F64)
+    if len(sizes) == 0:
+        return np.zeros(0)
+    x = np.asarray(q_abs, F64) @ np.asarray(means, F64).T * F64(scale) + np.log(sizes)
+    p = np.exp(x - x.max(axis=1, keepdims=True))
+    return (p / p.sum(axis=1, keepdims=True)).sum(axis=0)
+
+
+def block_select(scores, k: int, n_first: int, n_last: int):
+    """The k best blocks in rising order: the first n_first and last n_last
+    above all others (whatever their scores, by the lower index), then by
+    score, equal ones by the lower index, NaN last."""
+    n = len(scores)
+
+    def rank(j):
+        forced = j < n_first or j >= n - n_last
+        if forced:
+            return (0, 0.0, j)
+        return (2, 0.0, j) if scores[j] != scores[j] else (1, -float(scores[j]), j)
+    return sorted(sorted(range(n), key=rank)[:k])
+
+
+# ----------------------------------------------------------------------------
 # brute force (pure Python loops) for tiny inputs
 # ----------------------------------------------------------------------------
 
