@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(kSThreads, 1)
   const int ctx = ctx_len[b], nb = min(blocks_of(ctx), key_blocks);
   const bool work = tile * kScoreTile < nb;
   if (warp == 0) {
-    if (work && lane == 0) {
+    if (work && ptx::elect_one()) {
       ptx::tma_prefetch_desc(&mapQ);
       ptx::tma_prefetch_desc(&mapK);
       for (int c = 0; c < 9; ++c) {
@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(kSThreads, 1)
       }
     }
   } else if (warp == 1) {
-    if (work && lane == 0) {
+    if (work && ptx::elect_one()) {
       constexpr uint32_t id = idesc_bf16(128, kScoreTile, false, false);
       bool ok = true;
       for (int c = 0; c < 9 && ok; ++c) {

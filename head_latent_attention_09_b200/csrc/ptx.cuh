@@ -26,6 +26,23 @@ __device__ __forceinline__ unsigned long long globaltimer() {
   return t;
 }
 
+// One lane of a converged warp, for code that issues tcgen05 or TMA
+// instructions.  Under a branch on elect.sync the compiler keeps their operands
+// in uniform registers; under `lane == 0` it proves nothing and moves every
+// operand there one by one, which made a back-to-back tcgen05.mma cost ~124
+// cycles of issue instead of at most 64 (measured: a barrier wait, four pair
+// MMAs of N = 256 and a commit in 493 against 257 cycles, the latter being the
+// tensor pipe's own rate).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(e));
+  return e != 0;
+}
+
 // ---------------------------------------------------------------- mbarrier
 __device__ __forceinline__ void mbar_init(uint64_t *bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count) : "memory");

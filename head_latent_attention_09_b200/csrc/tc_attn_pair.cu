@@ -454,7 +454,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (ok && vpending) issue_v(vpc, vt0);
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issue
-    if (leader && lane == 0) {
+    const bool issuer = ptx::elect_one();
+    if (leader && issuer) {
       Walk w;
       walk_init(w, a, share);
       Piece pc;

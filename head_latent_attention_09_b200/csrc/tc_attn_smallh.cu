@@ -471,7 +471,7 @@ __global__ void __launch_bounds__(Cfg<H, F8>::kThreads, 1)
     }
   } else if (warp == 1) {
     // -------------------------------------------------------------- MMA issue
-    if (lane == 0) {
+    if (ptx::elect_one()) {
       constexpr uint32_t idS = idesc_bf16(128, H, false, false);
       constexpr uint32_t idO = idesc_bf16(128, H, true, false);
       Walk w;

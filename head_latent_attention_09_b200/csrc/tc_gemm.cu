@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   const uint32_t tmem = *tmem_slot;
 
   if (warp == 0) {
-    if (lane == 0) {
+    if (ptx::elect_one()) {
       const CUtensorMap *mA = use_a1 ? &mapA1 : &mapA0;
       const int a_m0 = use_a1 ? m0 - g.a_split_tile * 128 : m0;
       const uint32_t a_bytes = use_a1 ? (uint32_t)g.a1_rows * 128u : (uint32_t)kABytes;
@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
+    if (ptx::elect_one()) {
       constexpr uint32_t idesc = idesc_bf16(128, BN, A_MN, false);
       for (int gi = 0; gi < ngrp; ++gi) {
         const int s = gi % NG;
