@@ -31,10 +31,10 @@
 // sub-stages of 64 tokens x 128 columns (16 KB each), all through one ring of
 // 16 KB slots filled in the order the MMAs consume them.
 //
-// Warp roles per CTA (224 threads): warps 0 and 6 producers (TMA, and the
-// hand copy of a sequence's last partial block; each owns half the ring's
+// Warp roles per CTA (352 threads): warps 0 and 10 producers (TMA, and the
+// zeroes behind a sequence's last partial block; each owns half the ring's
 // slots), warp 1 tensor-memory allocation and (leader CTA only) MMA issue,
-// warps 2-5 softmax, O rescale and epilogue (one thread per tensor-memory
+// warps 2-9 softmax, O rescale and epilogue (two threads per tensor-memory
 // lane).
 //
 // Tree of drafted tokens (kTree): the query rows of a sequence are (drafted
@@ -59,15 +59,15 @@
 namespace mla {
 namespace {
 
-constexpr int kThreads = 224;
-// TMA producer warps 0 and 6.  A thread that issues cp.async.bulk.tensor
-// copies sustains about two copies per microsecond (about 31 GB/s of 16 KB
-// boxes, measured, from L2 or HBM alike), so two threads issue: each owns the
-// ring slots s with s % 2 == its index.  Warp 0 also loads Q.  (A third
-// producer warp measured slightly slower: it shares a sub-partition with a
-// softmax warp.)
+constexpr int kThreads = 352;
+constexpr int kSoftmaxWarps = 8;        // warps 2-9
+// TMA producer warps 0 and 10.  One warp that waits for a slot, arms its
+// barrier and issues a copy takes about 350 cycles a slot (measured: 48 B a
+// clock with 16 KB boxes out of L2), and the MMAs want a slot every 256, so two
+// warps issue: each owns the ring slots s with s % 2 == its index.  Warp 0 also
+// loads Q.
 constexpr int kProducers = 2;
-__device__ __forceinline__ int producer_index(int warp) { return warp == 0 ? 0 : (warp == 6 ? 1 : -1); }
+__device__ __forceinline__ int producer_index(int warp) { return warp == 0 ? 0 : (warp == 10 ? 1 : -1); }
 constexpr int kTileTok = 256;           // tokens per pair tile (MMA N of S = Q K^T)
 constexpr int kHalfTok = 128;           // tokens of a tile each CTA stages for S
 constexpr int kSubTok = 64;             // tokens per O += P V sub-stage
@@ -77,29 +77,25 @@ constexpr int kQBytes = 9 * 8192;       // 64 heads x 576 bf16, nine 64-column c
 constexpr int kPBytes = 4 * 8192;       // 64 heads x 256 tokens bf16, four 64-token chunks
 constexpr float kRescale = 8.0f;        // rescale O only when the running max grows by > 2^8
 
-// The evict-first L2 hint on a row's last read (the column-split V staging).
-#ifndef MLA_PAIR_EVICT
-#define MLA_PAIR_EVICT 1
-#endif
-
 constexpr int kOffQ = 0;
 constexpr int kOffRing = kOffQ + kQBytes;
 constexpr int kOffP = kOffRing + kSlots * kSlot;
-constexpr int kOffRed = kOffP + kPBytes;                // float red_m[2][128], red_l[128]
-constexpr int kOffBar = kOffRed + 3 * 128 * 4;
+constexpr int kOffRed = kOffP + kPBytes;                // float red_m[2][4][64], red_l[4][64]
+constexpr int kOffBar = kOffRed + 12 * 64 * 4;
 // barriers
-constexpr int kBarFull = 0;                     // [7] leader: 1 arrival + tx bytes of both CTAs
+constexpr int kBarFull = 0;                     // [7] leader: an arrival from each CTA + tx bytes of both
 constexpr int kBarEmpty = kBarFull + kSlots;    // [7] both: pair commit
 constexpr int kBarQFull = kBarEmpty + kSlots;   // leader: 1 arrival + tx
 constexpr int kBarQEmpty = kBarQFull + 1;       // both: pair commit
 constexpr int kBarSFull = kBarQEmpty + 1;       // [2] both: pair commit
-constexpr int kBarPFull = kBarSFull + 2;        // leader: 8 warp arrivals per tile
+constexpr int kBarPFull = kBarSFull + 2;        // leader: 16 warp arrivals per tile
 constexpr int kBarPFree = kBarPFull + 1;        // both: pair commit after each tile's P.V
 constexpr int kBarODone = kBarPFree + 1;        // [2] both: pair commit after P.V of even / odd tiles
-constexpr int kBarOFree = kBarODone + 2;        // leader: 8 warp arrivals
-constexpr int kBarXchg = kBarOFree + 1;         // [2] local: 4 softmax-warp arrivals (row-max exchange)
-constexpr int kBarLsum = kBarXchg + 2;          // local: 4 softmax-warp arrivals (row-sum exchange)
-constexpr int kNumBars = kBarLsum + 1;
+constexpr int kBarOFree = kBarODone + 2;        // leader: 16 warp arrivals
+constexpr int kBarXchg = kBarOFree + 1;         // [2] local: 8 softmax-warp arrivals (row-max exchange)
+constexpr int kBarLsum = kBarXchg + 2;          // local: 8 softmax-warp arrivals (row-sum exchange)
+constexpr int kBarEnd = kBarLsum + 1;           // [2] local: a producer's load of a sequence's last partial block
+constexpr int kNumBars = kBarEnd + kProducers;
 constexpr int kOffMisc = kOffBar + kNumBars * 8;
 constexpr int kSmemBytes = kOffMisc + 16;
 constexpr int kSmemAlloc = kSmemBytes + 1024;
@@ -179,16 +175,18 @@ __device__ __forceinline__ long long kv_row(const AttnArgs &a, const Piece &p, i
   return !kTree && a.sel ? selected_row(a, p.b, t, p.ctx) : token_row(a, p.b, t);
 }
 
+// The k lowest bits (none for k <= 0, all from 32 on).
+__device__ __forceinline__ uint32_t low_bits(int k) { return k <= 0 ? 0u : (k >= 32 ? 0xffffffffu : (1u << k) - 1u); }
+
 // Bits of word w (columns 32w .. 32w + 31) of a row's validity: column c holds
 // token base + c, valid below `cached` and, past it, where `bits` has the
 // drafted token's bit; `n` columns lie inside the piece.
 __device__ __forceinline__ uint32_t tree_valid(int w, int base, int n, int cached, unsigned long long bits) {
-  auto below = [](int k) { return k <= 0 ? 0u : (k >= 32 ? 0xffffffffu : (1u << k) - 1u); };
   const int sh = cached - base - 32 * w;     // column of the first drafted token within the word
   uint32_t d = 0;
   if (sh >= 0 && sh < 32) d = (uint32_t)(bits << sh);
   else if (sh < 0 && sh > -64) d = (uint32_t)(bits >> -sh);
-  return (below(sh) | d) & below(n - 32 * w);
+  return (low_bits(sh) | d) & low_bits(n - 32 * w);
 }
 
 struct Bars {
@@ -204,6 +202,7 @@ struct Bars {
   __device__ uint64_t *ofree() { return b + kBarOFree; }
   __device__ uint64_t *xchg(int i) { return b + kBarXchg + i; }
   __device__ uint64_t *lsum() { return b + kBarLsum; }
+  __device__ uint64_t *end(int p) { return b + kBarEnd + p; }
 };
 
 // Warp-uniform bounded wait: lane 0 waits, the result is broadcast, the other
@@ -249,8 +248,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   uint8_t *sQ = sm + kOffQ;
   uint8_t *sRing = sm + kOffRing;
   uint8_t *sP = sm + kOffP;
-  float *red_m = reinterpret_cast<float *>(sm + kOffRed);   // [2][128]
-  float *red_l = red_m + 256;                                // [128]
+  float *red_m = reinterpret_cast<float *>(sm + kOffRed);   // [2][4][64]
+  float *red_l = red_m + 512;                                // [4][64]
   Bars bars{reinterpret_cast<uint64_t *>(sm + kOffBar)};
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + kOffMisc);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + kOffMisc + 4);
@@ -263,7 +262,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kSlots; ++s) {
-      ptx::mbar_init(bars.full(s), 1);
+      ptx::mbar_init(bars.full(s), 2);
       ptx::mbar_init(bars.empty(s), 1);
     }
     ptx::mbar_init(bars.qfull(), 1);
@@ -271,12 +270,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(bars.sfull(i), 1);
       ptx::mbar_init(bars.odone(i), 1);
-      ptx::mbar_init(bars.xchg(i), 4);
+      ptx::mbar_init(bars.xchg(i), kSoftmaxWarps);
     }
-    ptx::mbar_init(bars.pfull(), 8);
+    for (int i = 0; i < kProducers; ++i) ptx::mbar_init(bars.end(i), 1);
+    ptx::mbar_init(bars.pfull(), 2 * kSoftmaxWarps);
     ptx::mbar_init(bars.pfree(), 1);
-    ptx::mbar_init(bars.ofree(), 8);
-    ptx::mbar_init(bars.lsum(), 4);
+    ptx::mbar_init(bars.ofree(), 2 * kSoftmaxWarps);
+    ptx::mbar_init(bars.lsum(), kSoftmaxWarps);
     *abort_flag = 0;
     ptx::fence_barrier_init();
   }
@@ -297,31 +297,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // Fill the ring in the order the MMAs consume it: the nine K chunks of
     // tile i, then the V sub-stages of tile i-1 (tiles counted across the
     // share's pieces).  Job j goes to slot j % kSlots, owned by producer
-    // (j % kSlots) % kProducers, so two threads keep TMA loads in flight at
+    // (j % kSlots) % kProducers, so two warps keep TMA loads in flight at
     // once, while every slot still has one producer that visits its jobs in
     // order: its empty barrier is never more than one phase behind the phase
-    // waited for (a parity wait cannot tell one phase behind from three).  Lane 0 issues TMA; the
-    // leader arms each slot with the bytes both CTAs' loads bring (the peer's
+    // waited for (a parity wait cannot tell one phase behind from three).  A
+    // slot's full barrier (the leader's) takes an arrival from each CTA; the
+    // leader's also arms it with the bytes both CTAs' loads bring (the peer's
     // loads count on the leader's barrier directly).  Warp 0 also loads Q.
     const int pid = producer_index(warp);
     const bool boxes64 = a.page_size != 0 || (!kTree && a.sel != nullptr);
     const uint32_t lq = ptx::leader_addr(bars.qfull());
     const uint32_t lf0 = ptx::leader_addr(bars.full(0));
-    if (lane == 0) {
+    if (ptx::elect_one()) {
       ptx::tma_prefetch_desc(&mapQ);
       ptx::tma_prefetch_desc(&mapK);
       ptx::tma_prefetch_desc(&mapV);
       ptx::tma_prefetch_desc(&mapV2);
+      if (kTree) ptx::tma_prefetch_desc(&mapT);
     }
     Walk w;
     walk_init(w, a, share);
-#if MLA_PAIR_EVICT
     const uint64_t last_read = ptx::l2_policy_evict_first();
-#endif
     Piece pc, vpc;            // vpc/vt0: the tile whose V sub-stages are pending
     int vt0 = 0;
     bool vpending = false;
-    int sc = 0, npc = 0;
+    int npc = 0, nend = 0;
     bool ok = true;
     int ws_ = 0;               // ring slot of the next job
     int wround = 0;            // how many times the ring has been filled before
@@ -336,76 +336,69 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ++wround;
       }
       if (s % kProducers != pid) return -2;
-      bool got = true;
-      if (lane == 0 && r > 0) got = ptx::mbar_wait(bars.empty(s), (r - 1) & 1, a.status, abort_flag);
-      got = __shfl_sync(0xffffffffu, got ? 1 : 0, 0) != 0;
-      __syncwarp();
-      return got ? s : -1;
+      if (r > 0 && !warp_wait(bars.empty(s), (r - 1) & 1, a.status, abort_flag)) return -1;
+      return s;
+    };
+    // Before a slot's loads (one lane): this CTA's arrival on its full barrier.
+    auto arm = [&](int s) {
+      if (leader) ptx::mbar_arrive_expect_tx(bars.full(s), 2 * kSlot);
+      else ptx::mbar_arrive_remote_addr(lf0 + 8 * s);
     };
     // V sub-stages of the tile at token t0 of piece p: tokens t0 + 64t..,
-    // latent columns 256g + 128 * rank .. +128.
+    // latent columns 256g + 128 * rank .. +128, one 3D box: 64 rows x both
+    // 64-column chunks (chunk index feat0 / 64).
     auto issue_v = [&](const Piece &p, int t0) -> bool {
       const int nsub = tile_subs(p, t0);
       for (int t = 0; t < nsub; ++t) {
+        const int tok0 = t0 + kSubTok * t;
+        // a tree's last blocks come from their copy
+        const bool copied = kTree && tok0 + kSubTok > p.cached;
+        const bool partial = !kTree && tok0 + kSubTok > p.ctx;
+        const CUtensorMap *map = copied ? &mapT : &mapV2;
+        int y = -1;
         for (int g = 0; g < 2; ++g) {
           const int s = acquire();
           if (s == -2) continue;
           if (s < 0) return false;
           uint8_t *dst = sRing + s * kSlot;
-          const int tok0 = t0 + kSubTok * t;
-          if (!kTree && tok0 + kSubTok > p.ctx) {
-            // The block runs past the sequence: the leader copies the valid
-            // rows of both CTAs' column halves by hand and zeroes the rest,
-            // so that no unwritten cache row (possibly NaN) reaches P.V.
-            // 128-byte rows, 16-byte units swizzled by row (the layout a
-            // 128-byte-swizzled TMA load produces).  The peer skips it.
-            if (leader) {
-              const uint32_t own = ptx::smem_u32(dst), peer = ptx::mapa_peer(own, 1);
-              for (int u = lane; u < 2 * 2 * 64 * 8; u += 32) {
-                const int cta = u >> 10, half = (u >> 9) & 1, row = (u >> 3) & 63, c = u & 7;
-                const int tk = tok0 + row;
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (tk < p.ctx) {
-                  const long long r = kv_row<kTree>(a, p, tk);
-                  if (r >= 0)
-                    v = *reinterpret_cast<const uint4 *>(reinterpret_cast<const __nv_bfloat16 *>(a.cache) +
-                                                         r * 576 + 256 * g + 128 * cta + 64 * half + 8 * c);
-                  else
-                    atomicOr(a.status, kStatusBounds);
-                }
-                const uint32_t off = half * 8192 + row * 128 + ((c ^ (row & 7)) << 4);
-                ptx::st_shared_cluster_v4(cta ? peer + off : own + off, v);
-              }
-              ptx::fence_acq_rel_cluster();
-              ptx::fence_proxy_async_cluster();
-              __syncwarp();
-              if (lane == 0) ptx::mbar_arrive(bars.full(s));
+          const int chunk0 = 4 * g + 2 * (int)rank;
+          if (y < 0)
+            y = copied ? p.b * kTreeCopyRows + tok0 - p.cached / kTile * kTile
+                       : block_row<kTree>(a, p, tok0, kv_rows);
+          if (!partial) {
+            if (ptx::elect_one()) {
+              arm(s);
+              ptx::tma_load_3d_pair_hint(dst, map, lf0 + 8 * s, 0, y, chunk0, last_read);
             }
-          } else if (lane == 0) {
-            // a tree's last blocks come from their copy
-            const bool copied = kTree && tok0 + kSubTok > p.cached;
-            const int y = copied ? p.b * kTreeCopyRows + tok0 - p.cached / kTile * kTile
-                                 : block_row<kTree>(a, p, tok0, kv_rows);
-            const CUtensorMap *map = copied ? &mapT : &mapV2;
-            if (leader) ptx::mbar_arrive_expect_tx(bars.full(s), 2 * kSlot);
-            const int feat0 = 256 * g + 128 * (int)rank;
-            // one 3D box: 64 rows x both 64-column chunks (chunk index feat0 / 64)
-#if MLA_PAIR_EVICT
-            ptx::tma_load_3d_pair_hint(dst, map, lf0 + 8 * s, 0, y, feat0 / 64, last_read);
-#else
-            ptx::tma_load_3d_pair(dst, map, lf0 + 8 * s, 0, y, feat0 / 64);
-#endif
+            __syncwarp();
+            continue;
           }
-          ++sc;
+          // The block runs past the sequence: its load completes on a barrier
+          // of this warp's, which zeroes the rows past the end, so that no
+          // unwritten cache row (possibly NaN) reaches P.V, and then arrives
+          // for its CTA without any bytes.
+          if (ptx::elect_one()) {
+            ptx::mbar_arrive_expect_tx(bars.end(pid), kSlot);
+            ptx::tma_load_3d(dst, map, bars.end(pid), 0, y, chunk0);
+          }
+          __syncwarp();
+          if (!warp_wait(bars.end(pid), nend & 1, a.status, abort_flag)) return false;
+          ++nend;
+          const int row0 = p.ctx - tok0;
+          for (int u = lane; u < (64 - row0) * 16; u += 32)
+            *reinterpret_cast<uint4 *>(dst + (u & 8) * 1024 + (row0 + (u >> 4)) * 128 + (u & 7) * 16) =
+                make_uint4(0, 0, 0, 0);
+          ptx::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive_remote_addr(lf0 + 8 * s);
         }
       }
       return true;
     };
     while (ok && walk_next<kTree>(w, a, share, pc)) {
-      bool qok = true;
-      if (lane == 0) {
-        if (pid == 0 && npc > 0) qok = ptx::mbar_wait(bars.qempty(), (npc - 1) & 1, a.status, abort_flag);
-        if (pid == 0 && qok) {
+      if (pid == 0) {
+        if (npc > 0 && !warp_wait(bars.qempty(), (npc - 1) & 1, a.status, abort_flag)) break;
+        if (ptx::elect_one()) {
           if (leader) ptx::mbar_arrive_expect_tx(bars.qfull(), 2 * kQBytes);
           for (int c = 0; c < 9; ++c) {
             if (kTree)   // rows past the sequence's are zero-filled
@@ -415,24 +408,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               ptx::tma_load_2d_pair(sQ + c * 8192, &mapQ, lq, 64 * c, pc.b * 128 + 64 * (int)rank);
           }
         }
+        __syncwarp();
       }
-      if (!__shfl_sync(0xffffffffu, qok ? 1 : 0, 0)) break;
       for (int k = 0; k < pc.ntiles && ok; ++k) {
         // K chunks of this tile: this CTA's 128 tokens x 64 columns each.
         const int t0 = pc.tok_begin + kTileTok * k;
         const int tr = t0 + kHalfTok * (int)rank;
-        int y0 = 0, y1 = 0;
-        if (lane == 0) {
-          y0 = block_row<kTree>(a, pc, tr, kv_rows);
-          if (boxes64) y1 = block_row<kTree>(a, pc, tr + kSubTok, kv_rows);
-        }
+        const int y0 = block_row<kTree>(a, pc, tr, kv_rows);
+        const int y1 = boxes64 ? block_row<kTree>(a, pc, tr + kSubTok, kv_rows) : 0;
         for (int c = 0; c < 9; ++c) {
           const int s = acquire();
           if (s == -2) continue;
           if (s < 0) { ok = false; break; }
-          if (lane == 0) {
+          if (ptx::elect_one()) {
             uint8_t *dst = sRing + s * kSlot;
-            if (leader) ptx::mbar_arrive_expect_tx(bars.full(s), 2 * kSlot);
+            arm(s);
             if (!boxes64) {
               ptx::tma_load_2d_pair(dst, &mapK, lf0 + 8 * s, 64 * c, y0);
             } else {
@@ -441,7 +431,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               ptx::tma_load_2d_pair(dst + 8192, &mapV, lf0 + 8 * s, 64 * c, y1);
             }
           }
-          ++sc;
+          __syncwarp();
         }
         if (!ok) break;
         if (vpending && !issue_v(vpc, vt0)) { ok = false; break; }
@@ -544,15 +534,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   } else {
     // ------------------------------------------- softmax, rescale, epilogue
-    const int q = warp & 3;
-    const int l = q * 32 + lane;          // tensor-memory lane of this thread
-    const int h = l & 63, th = l >> 6;    // local head, token half
+    // Two warps to a tensor-memory quadrant: thread (l, hf) owns lane l, i.e.
+    // local head h and token half th, and columns 64 hf .. of that half's 128
+    // scores: token chunk part = 2 th + hf of the tile.  A head's row is held
+    // by four threads, which exchange their maxima and sums through shared
+    // memory.
+    const int q = warp & 3, hf = (warp - 2) >> 2;
+    const int l = q * 32 + lane;
+    const int h = l & 63, th = l >> 6, part = 2 * th + hf;
     const uint32_t lane_addr = tmem + ((uint32_t)(q * 32) << 16);
+    const uint32_t o_addr = lane_addr + kColO + 128 * hf;   // latent columns 256 hf + 128 th ..
     const uint32_t leader_pfull = ptx::leader_addr(bars.pfull());
     const uint32_t leader_ofree = ptx::leader_addr(bars.ofree());
     float *opart = reinterpret_cast<float *>(a.ws + a.L.opart_off);
     float *lse_out = reinterpret_cast<float *>(a.ws + a.L.lse_off);
-    uint8_t *prow = sP + h * 128;         // row h of each 64-token P chunk
+    uint8_t *prow = sP + part * 8192 + h * 128;   // this row of the thread's 64-token P chunk
     Walk w;
     walk_init(w, a, share);
     Piece pc;
@@ -568,39 +564,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (a.tree.T < 64) bits &= (1ull << a.tree.T) - 1ull;
       }
       for (int k = 0; k < pc.ntiles; ++k, ++i) {
-        const int base = pc.tok_begin + kTileTok * k + kHalfTok * th;
-        const int nvalid = min(max(pc.tok_end - base, 0), kHalfTok);
-        const uint32_t scol = lane_addr + (i & 1) * kColS;
+        const int base = pc.tok_begin + kTileTok * k + 64 * part;
+        const int nvalid = min(max(pc.tok_end - base, 0), 64);
         if (!warp_wait(bars.sfull(i & 1), (i >> 1) & 1, a.status, abort_flag)) { ok = false; break; }
         ptx::tc_fence_after();
-        // This row's 128 scores, in log2 units, invalid tokens at -inf.
-        float v[kHalfTok];
-        ptx::tmem_ld64_sync(scol, reinterpret_cast<uint32_t *>(v));
-        ptx::tmem_ld64_sync(scol + 64, reinterpret_cast<uint32_t *>(v) + 64);
+        // This thread's 64 scores, in log2 units, invalid tokens at -inf.
+        float v[64];
+        ptx::tmem_ld64_sync(lane_addr + (i & 1) * kColS + 64 * hf, reinterpret_cast<uint32_t *>(v));
         float mx[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
-        if (kTree) {
-          uint32_t ok[4];
+        if (base + 64 <= (kTree ? min(pc.cached, pc.tok_end) : pc.tok_end)) {
 #pragma unroll
-          for (int w4 = 0; w4 < 4; ++w4)
-            ok[w4] = base + kHalfTok <= pc.cached ? 0xffffffffu : tree_valid(w4, base, nvalid, pc.cached, bits);
-#pragma unroll
-          for (int j = 0; j < kHalfTok; ++j) {
-            v[j] = (ok[j >> 5] >> (j & 31)) & 1u ? v[j] * a.scale_log2 : -CUDART_INF_F;
+          for (int j = 0; j < 64; ++j) {
+            v[j] *= a.scale_log2;
             mx[j & 3] = fmaxf(mx[j & 3], v[j]);
           }
         } else {
+          uint32_t valid[2];
 #pragma unroll
-          for (int j = 0; j < kHalfTok; ++j) {
-            v[j] = j < nvalid ? v[j] * a.scale_log2 : -CUDART_INF_F;
+          for (int w2 = 0; w2 < 2; ++w2)
+            valid[w2] = kTree ? tree_valid(w2, base, nvalid, pc.cached, bits) : low_bits(nvalid - 32 * w2);
+#pragma unroll
+          for (int j = 0; j < 64; ++j) {
+            v[j] = (valid[j >> 5] >> (j & 31)) & 1u ? v[j] * a.scale_log2 : -CUDART_INF_F;
             mx[j & 3] = fmaxf(mx[j & 3], v[j]);
           }
         }
         const float mloc = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        red_m[(i & 1) * 128 + l] = mloc;
+        float *rm = red_m + (i & 1) * 256;
+        rm[part * 64 + h] = mloc;
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(bars.xchg(i & 1));
         if (!warp_wait(bars.xchg(i & 1), (i >> 1) & 1, a.status, abort_flag)) { ok = false; break; }
-        const float m_tile = fmaxf(mloc, red_m[(i & 1) * 128 + (l ^ 64)]);
+        const float m_tile = fmaxf(fmaxf(rm[h], rm[64 + h]), fmaxf(rm[128 + h], rm[192 + h]));
         bool rescale = false;
         float alpha = 1.f;
         if (m_tile > m_run + kRescale) {
@@ -611,32 +606,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         // Probabilities (bf16 pairs) and their sum, before waiting for the
         // previous tile's P.V, so that only the store below waits for it.
+        // P is rounded to bf16 because the MMA takes both operands in one
+        // 16-bit type and V is bf16; the sum is of the unrounded values.
         // A row with nothing valid so far (a tree's masks) subtracts 0: -inf - -inf is NaN.
         const float m_use = kTree && m_run == -CUDART_INF_F ? 0.f : m_run;
-        uint32_t pk[kHalfTok / 2];
-        float ps[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        uint32_t pk[32];
+        float ps[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int j = 0; j < kHalfTok / 2; ++j) {
+        for (int j = 0; j < 32; ++j) {
           const float p0 = ptx::exp2_approx(v[2 * j] - m_use), p1 = ptx::exp2_approx(v[2 * j + 1] - m_use);
-          ps[j & 7] += p0 + p1;
+          ps[j & 3] += p0 + p1;
           __nv_bfloat162 b2 = __floats2bfloat162_rn(p0, p1);
           pk[j] = *reinterpret_cast<uint32_t *>(&b2);
         }
-        const float sum = ((ps[0] + ps[1]) + (ps[2] + ps[3])) + ((ps[4] + ps[5]) + (ps[6] + ps[7]));
+        l_part += (ps[0] + ps[1]) + (ps[2] + ps[3]);
         // P of the previous tile must have been read by its P.V.
         if (i >= 1 && !warp_wait(bars.pfree(), (i - 1) & 1, a.status, abort_flag)) { ok = false; break; }
-        // Tokens 128 th + 16c.. are 16-byte units 2(c&3), 2(c&3)+1 of row h of
-        // P chunk 2 th + (c >> 2) (128-byte swizzle by row).
+        // Tokens 8u .. of the chunk are 16-byte unit u of row h (128-byte swizzle by row).
 #pragma unroll
-        for (int c = 0; c < kHalfTok / 16; ++c) {
-          uint8_t *chunk = prow + (2 * th + (c >> 2)) * 8192;
-          const int u0 = 2 * (c & 3);
-          *reinterpret_cast<uint4 *>(chunk + ((u0 ^ (h & 7)) << 4)) =
-              make_uint4(pk[8 * c], pk[8 * c + 1], pk[8 * c + 2], pk[8 * c + 3]);
-          *reinterpret_cast<uint4 *>(chunk + (((u0 + 1) ^ (h & 7)) << 4)) =
-              make_uint4(pk[8 * c + 4], pk[8 * c + 5], pk[8 * c + 6], pk[8 * c + 7]);
-        }
-        l_part += sum;
+        for (int u = 0; u < 8; ++u)
+          *reinterpret_cast<uint4 *>(prow + ((u ^ (h & 7)) << 4)) =
+              make_uint4(pk[4 * u], pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]);
         // The rescale (tensor-memory loads and stores, .sync.aligned) is done by
         // the whole warp when any of its rows needs it; other rows use alpha = 1.
         if (__any_sync(0xffffffffu, rescale)) {
@@ -648,13 +638,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (!warp_wait(bars.odone((i - 1) & 1), ((i - 1) >> 1) & 1, a.status, abort_flag)) { ok = false; break; }
           ptx::tc_fence_after();
 #pragma unroll 1
-          for (int c = 0; c < 16; ++c) {
+          for (int c = 0; c < 8; ++c) {
             uint32_t r[16];
-            ptx::tmem_ld16(lane_addr + kColO + 16 * c, r);
+            ptx::tmem_ld16(o_addr + 16 * c, r);
             ptx::tmem_ld_wait();
 #pragma unroll
             for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * alpha);
-            ptx::tmem_st16(lane_addr + kColO + 16 * c, r);
+            ptx::tmem_st16(o_addr + 16 * c, r);
           }
           ptx::tmem_st_wait();
         }
@@ -665,18 +655,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       // ---- epilogue of the piece: O / l and the log-sum-exp
-      red_l[l] = l_part;
+      red_l[part * 64 + h] = l_part;
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(bars.lsum());
       if (!warp_wait(bars.lsum(), npc_s & 1, a.status, abort_flag)) { ok = false; break; }
       ++npc_s;
-      const float lsum = l_part + red_l[l ^ 64];
+      const float lsum = (red_l[h] + red_l[64 + h]) + (red_l[128 + h] + red_l[192 + h]);
       if (!warp_wait(bars.odone((i - 1) & 1), ((i - 1) >> 1) & 1, a.status, abort_flag)) { ok = false; break; }
       ptx::tc_fence_after();
       const int head = 64 * (int)rank + h;
       // a tree's row that attends nothing is zero, a NaN sum stays NaN
-      const float inv = (kTree ? lsum != 0.f : lsum > 0.f) ? 1.f / lsum : 0.f;
-      const float z = (kTree ? lsum != 0.f : lsum > 0.f) ? (m_run + log2f(lsum)) * 0.69314718055994531f : -CUDART_INF_F;
+      const bool some = kTree ? lsum != 0.f : lsum > 0.f;
+      const float inv = some ? 1.f / lsum : 0.f;
+      const float z = some ? (m_run + log2f(lsum)) * 0.69314718055994531f : -CUDART_INF_F;
       long long slot = pc.piece;
       bool whole = false;
       if (kTree) {
@@ -684,40 +675,68 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         whole = t.whole;
         slot = t.slot;
       }
-      float *dst = opart + part_row(a.L, slot, head) * (long long)a.d_c + 128 * th;
-      const long long orow = (long long)pc.b * a.tree.seq_rows + row;
-      __nv_bfloat16 *out = reinterpret_cast<__nv_bfloat16 *>(a.tree.out) + orow * a.d_c + 128 * th;
+      if (hf == 0 && th == 0 && !(kTree && row >= a.tree.seq_rows)) {
+        if (!whole) lse_out[part_row(a.L, slot, head)] = z;
+        else if (a.tree.lse) a.tree.lse[(long long)pc.b * a.tree.seq_rows + row] = z;
+      }
+      // The warp's 32 rows x 128 columns pass through shared memory 128 bytes
+      // of every row at a time (its 4 KB of the P buffer, which no P.V reads
+      // any more; the next P is stored only after all eight warps have met at
+      // a row-maximum exchange), so that a store instruction writes whole
+      // 128-byte lines of four rows, not 16 bytes of 32 rows (a piece's
+      // epilogue 7 -> 2.5 us).  16-byte units are swizzled by row.
+      uint8_t *stage = sP + (warp - 2) * 4096;
+      const int col0 = 256 * hf + 128 * th;
+      const int r0 = 64 * (int)rank + (q & 1) * 32;   // first head / row of the warp within the 128
+      if (kTree && whole) {
+        __nv_bfloat16 *out = reinterpret_cast<__nv_bfloat16 *>(a.tree.out);
+        const int g0 = 128 * (pc.v - pc.b * a.tree.groups) + r0;
 #pragma unroll 1
-      for (int c = 0; c < 16; ++c) {
-        uint32_t r[16];
-        ptx::tmem_ld16(lane_addr + kColO + 16 * c, r);
-        ptx::tmem_ld_wait();
-        if (kTree && whole) {
-          if (row < a.tree.seq_rows) {
-            uint32_t o[8];
+        for (int c = 0; c < 2; ++c) {
+          float v[64];
+          ptx::tmem_ld64_sync(o_addr + 64 * c, reinterpret_cast<uint32_t *>(v));
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const __nv_bfloat162 b2 =
-                  __floats2bfloat162_rn(__uint_as_float(r[2 * j]) * inv, __uint_as_float(r[2 * j + 1]) * inv);
+          for (int u = 0; u < 8; ++u) {
+            uint32_t o[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const __nv_bfloat162 b2 = __floats2bfloat162_rn(v[8 * u + 2 * j] * inv, v[8 * u + 2 * j + 1] * inv);
               o[j] = *reinterpret_cast<const uint32_t *>(&b2);
             }
-            uint4 *d = reinterpret_cast<uint4 *>(out + (c >> 3) * 256 + (c & 7) * 16);
-            d[0] = make_uint4(o[0], o[1], o[2], o[3]);
-            d[1] = make_uint4(o[4], o[5], o[6], o[7]);
+            *reinterpret_cast<uint4 *>(stage + lane * 128 + ((u ^ (lane & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
           }
-          continue;
-        }
-        if (kTree && row >= a.tree.seq_rows) continue;
-        float *d = dst + (c >> 3) * 256 + (c & 7) * 16;
+          __syncwarp();
 #pragma unroll
-        for (int j = 0; j < 16; j += 4)
-          *reinterpret_cast<float4 *>(d + j) =
-              make_float4(__uint_as_float(r[j]) * inv, __uint_as_float(r[j + 1]) * inv,
-                          __uint_as_float(r[j + 2]) * inv, __uint_as_float(r[j + 3]) * inv);
-      }
-      if (th == 0 && !(kTree && row >= a.tree.seq_rows)) {
-        if (!whole) lse_out[part_row(a.L, slot, head)] = z;
-        else if (a.tree.lse) a.tree.lse[orow] = z;
+          for (int it = 0; it < 8; ++it) {
+            const int r = 4 * it + (lane >> 3), u = lane & 7;
+            const uint4 x = *reinterpret_cast<const uint4 *>(stage + r * 128 + ((u ^ (r & 7)) << 4));
+            if (g0 + r < a.tree.seq_rows)
+              *reinterpret_cast<uint4 *>(out + ((long long)pc.b * a.tree.seq_rows + g0 + r) * a.d_c + col0 + 64 * c +
+                                         8 * u) = x;
+          }
+          __syncwarp();
+        }
+      } else {
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          uint32_t v[32];
+          ptx::tmem_ld16(o_addr + 32 * c, *reinterpret_cast<uint32_t(*)[16]>(v));
+          ptx::tmem_ld16(o_addr + 32 * c + 16, *reinterpret_cast<uint32_t(*)[16]>(v + 16));
+          ptx::tmem_ld_wait();
+#pragma unroll
+          for (int u = 0; u < 8; ++u)
+            *reinterpret_cast<float4 *>(stage + lane * 128 + ((u ^ (lane & 7)) << 4)) =
+                make_float4(__uint_as_float(v[4 * u]) * inv, __uint_as_float(v[4 * u + 1]) * inv,
+                            __uint_as_float(v[4 * u + 2]) * inv, __uint_as_float(v[4 * u + 3]) * inv);
+          __syncwarp();
+#pragma unroll
+          for (int it = 0; it < 8; ++it) {
+            const int r = 4 * it + (lane >> 3), u = lane & 7;
+            *reinterpret_cast<float4 *>(opart + part_row(a.L, slot, r0 + r) * (long long)a.d_c + col0 + 32 * c + 4 * u) =
+                *reinterpret_cast<const float4 *>(stage + r * 128 + ((u ^ (r & 7)) << 4));
+          }
+          __syncwarp();
+        }
       }
       ptx::tc_fence_before();
       __syncwarp();
