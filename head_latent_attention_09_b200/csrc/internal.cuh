@@ -307,11 +307,11 @@ __device__ __forceinline__ int plan_cached(const AttnArgs &a, int b) {
 // address), or -1 when its page is unmapped or outside the pool.
 __device__ __forceinline__ long long token_row(const AttnArgs &a, int b, long long t) {
   if (a.page_size == 0) return t < a.cache_len ? (long long)b * a.cache_len + t : -1;
-  const long long bi = t / a.page_size;
-  if (bi >= a.max_blocks) return -1;
+  const unsigned bi = (unsigned)t / (unsigned)a.page_size;   // t is a position: 31 bits
+  if (bi >= (unsigned)a.max_blocks) return -1;
   const int blk = a.block_table[(long long)b * a.max_blocks + bi];
   if (blk < 0 || blk >= a.cache_len) return -1;
-  return (long long)blk * a.page_size + t % a.page_size;
+  return (long long)blk * a.page_size + ((unsigned)t - bi * (unsigned)a.page_size);
 }
 
 // The same for token t of a sequence's selected blocks.  -1 also for a block

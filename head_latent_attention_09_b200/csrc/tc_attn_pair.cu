@@ -31,11 +31,10 @@
 // sub-stages of 64 tokens x 128 columns (16 KB each), all through one ring of
 // 16 KB slots filled in the order the MMAs consume them.
 //
-// Warp roles per CTA (352 threads): warps 0 and 10 producers (TMA, and the
-// zeroes behind a sequence's last partial block; each owns half the ring's
-// slots), warp 1 tensor-memory allocation and (leader CTA only) MMA issue,
-// warps 2-9 softmax, O rescale and epilogue (two threads per tensor-memory
-// lane).
+// Warp roles per CTA (352 threads): warp 0 TMA producer, warp 1
+// tensor-memory allocation and (leader CTA only) MMA issue, warps 2-9 softmax,
+// O rescale and epilogue (two threads per tensor-memory lane), warp 10 the
+// zeroes behind a sequence's last partial block.
 //
 // Tree of drafted tokens (kTree): the query rows of a sequence are (drafted
 // token, head), any number of them, cut into groups of 128; a group takes the
@@ -61,13 +60,7 @@ namespace {
 
 constexpr int kThreads = 352;
 constexpr int kSoftmaxWarps = 8;        // warps 2-9
-// TMA producer warps 0 and 10.  One warp that waits for a slot, arms its
-// barrier and issues a copy takes about 350 cycles a slot (measured: 48 B a
-// clock with 16 KB boxes out of L2), and the MMAs want a slot every 256, so two
-// warps issue: each owns the ring slots s with s % 2 == its index.  Warp 0 also
-// loads Q.
-constexpr int kProducers = 2;
-__device__ __forceinline__ int producer_index(int warp) { return warp == 0 ? 0 : (warp == 10 ? 1 : -1); }
+constexpr int kHelperWarp = 10;
 constexpr int kTileTok = 256;           // tokens per pair tile (MMA N of S = Q K^T)
 constexpr int kHalfTok = 128;           // tokens of a tile each CTA stages for S
 constexpr int kSubTok = 64;             // tokens per O += P V sub-stage
@@ -94,10 +87,10 @@ constexpr int kBarODone = kBarPFree + 1;        // [2] both: pair commit after P
 constexpr int kBarOFree = kBarODone + 2;        // leader: 16 warp arrivals
 constexpr int kBarXchg = kBarOFree + 1;         // [2] local: 8 softmax-warp arrivals (row-max exchange)
 constexpr int kBarLsum = kBarXchg + 2;          // local: 8 softmax-warp arrivals (row-sum exchange)
-constexpr int kBarEnd = kBarLsum + 1;           // [2] local: a producer's load of a sequence's last partial block
-constexpr int kNumBars = kBarEnd + kProducers;
+constexpr int kBarEnd = kBarLsum + 1;           // [2] local: the loads of a sequence's last partial block
+constexpr int kNumBars = kBarEnd + 2;
 constexpr int kOffMisc = kOffBar + kNumBars * 8;
-constexpr int kSmemBytes = kOffMisc + 16;
+constexpr int kSmemBytes = kOffMisc + 32;
 constexpr int kSmemAlloc = kSmemBytes + 1024;
 static_assert(kSmemAlloc <= 232448, "shared memory budget");
 static_assert(kOffRing % 1024 == 0 && kOffP % 1024 == 0 && kSlot % 1024 == 0,
@@ -202,7 +195,7 @@ struct Bars {
   __device__ uint64_t *ofree() { return b + kBarOFree; }
   __device__ uint64_t *xchg(int i) { return b + kBarXchg + i; }
   __device__ uint64_t *lsum() { return b + kBarLsum; }
-  __device__ uint64_t *end(int p) { return b + kBarEnd + p; }
+  __device__ uint64_t *end(int g) { return b + kBarEnd + g; }
 };
 
 // Warp-uniform bounded wait: lane 0 waits, the result is broadcast, the other
@@ -253,6 +246,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   Bars bars{reinterpret_cast<uint64_t *>(sm + kOffBar)};
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + kOffMisc);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + kOffMisc + 4);
+  int *end_slot = reinterpret_cast<int *>(sm + kOffMisc + 8);   // [2] ring slots of a last partial block
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = ptx::cluster_ctarank();
@@ -272,7 +266,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       ptx::mbar_init(bars.odone(i), 1);
       ptx::mbar_init(bars.xchg(i), kSoftmaxWarps);
     }
-    for (int i = 0; i < kProducers; ++i) ptx::mbar_init(bars.end(i), 1);
+    for (int i = 0; i < 2; ++i) ptx::mbar_init(bars.end(i), 1);
     ptx::mbar_init(bars.pfull(), 2 * kSoftmaxWarps);
     ptx::mbar_init(bars.pfree(), 1);
     ptx::mbar_init(bars.ofree(), 2 * kSoftmaxWarps);
@@ -292,156 +286,159 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   // the query and the cache it wrote are read.
   pdl_wait();
 
-  if (producer_index(warp) >= 0) {
-    // -------------------------------------------------------------- producers
-    // Fill the ring in the order the MMAs consume it: the nine K chunks of
+  if (warp == 0) {
+    // --------------------------------------------------------------- producer
+    // Fills the ring in the order the MMAs consume it: the nine K chunks of
     // tile i, then the V sub-stages of tile i-1 (tiles counted across the
-    // share's pieces).  Job j goes to slot j % kSlots, owned by producer
-    // (j % kSlots) % kProducers, so two warps keep TMA loads in flight at
-    // once, while every slot still has one producer that visits its jobs in
-    // order: its empty barrier is never more than one phase behind the phase
-    // waited for (a parity wait cannot tell one phase behind from three).  A
-    // slot's full barrier (the leader's) takes an arrival from each CTA; the
-    // leader's also arms it with the bytes both CTAs' loads bring (the peer's
-    // loads count on the leader's barrier directly).  Warp 0 also loads Q.
-    const int pid = producer_index(warp);
-    const bool boxes64 = a.page_size != 0 || (!kTree && a.sel != nullptr);
-    const uint32_t lq = ptx::leader_addr(bars.qfull());
-    const uint32_t lf0 = ptx::leader_addr(bars.full(0));
+    // share's pieces).  A slot's full barrier (the leader's) takes an arrival
+    // from each CTA; the leader's also arms it with the bytes both CTAs' loads
+    // bring (the peer's loads count on the leader's barrier directly).  One
+    // elected thread does it all, in few instructions a slot (the MMAs want
+    // one every 256 cycles): a tile's four cache rows are looked up once, for
+    // the tile after the one being loaded, so that a paged cache's table reads
+    // are not waited for.
     if (ptx::elect_one()) {
+      const bool boxes64 = a.page_size != 0 || (!kTree && a.sel != nullptr);
+      const uint32_t lq = ptx::leader_addr(bars.qfull());
+      const uint32_t lf0 = ptx::leader_addr(bars.full(0));
       ptx::tma_prefetch_desc(&mapQ);
       ptx::tma_prefetch_desc(&mapK);
       ptx::tma_prefetch_desc(&mapV);
       ptx::tma_prefetch_desc(&mapV2);
       if (kTree) ptx::tma_prefetch_desc(&mapT);
-    }
-    Walk w;
-    walk_init(w, a, share);
-    const uint64_t last_read = ptx::l2_policy_evict_first();
-    Piece pc, vpc;            // vpc/vt0: the tile whose V sub-stages are pending
-    int vt0 = 0;
-    bool vpending = false;
-    int npc = 0, nend = 0;
-    bool ok = true;
-    int ws_ = 0;               // ring slot of the next job
-    int wround = 0;            // how many times the ring has been filled before
-    // Next ring job: returns its slot if this warp owns it (after waiting,
-    // in round r >= 1, until the MMAs of round r-1 released it), -2 if the
-    // other producer owns it, -1 on a failed wait.  Warp-uniform.
-    auto acquire = [&]() -> int {
-      const int s = ws_;
-      const int r = wround;
-      if (++ws_ == kSlots) {
-        ws_ = 0;
-        ++wround;
-      }
-      if (s % kProducers != pid) return -2;
-      if (r > 0 && !warp_wait(bars.empty(s), (r - 1) & 1, a.status, abort_flag)) return -1;
-      return s;
-    };
-    // Before a slot's loads (one lane): this CTA's arrival on its full barrier.
-    auto arm = [&](int s) {
-      if (leader) ptx::mbar_arrive_expect_tx(bars.full(s), 2 * kSlot);
-      else ptx::mbar_arrive_remote_addr(lf0 + 8 * s);
-    };
-    // V sub-stages of the tile at token t0 of piece p: tokens t0 + 64t..,
-    // latent columns 256g + 128 * rank .. +128, one 3D box: 64 rows x both
-    // 64-column chunks (chunk index feat0 / 64).
-    auto issue_v = [&](const Piece &p, int t0) -> bool {
-      const int nsub = tile_subs(p, t0);
-      for (int t = 0; t < nsub; ++t) {
-        const int tok0 = t0 + kSubTok * t;
-        // a tree's last blocks come from their copy
-        const bool copied = kTree && tok0 + kSubTok > p.cached;
-        const bool partial = !kTree && tok0 + kSubTok > p.ctx;
-        const CUtensorMap *map = copied ? &mapT : &mapV2;
-        int y = -1;
-        for (int g = 0; g < 2; ++g) {
-          const int s = acquire();
-          if (s == -2) continue;
-          if (s < 0) return false;
-          uint8_t *dst = sRing + s * kSlot;
-          const int chunk0 = 4 * g + 2 * (int)rank;
-          if (y < 0)
-            y = copied ? p.b * kTreeCopyRows + tok0 - p.cached / kTile * kTile
-                       : block_row<kTree>(a, p, tok0, kv_rows);
-          if (!partial) {
-            if (ptx::elect_one()) {
-              arm(s);
-              ptx::tma_load_3d_pair_hint(dst, map, lf0 + 8 * s, 0, y, chunk0, last_read);
+      Walk w;
+      walk_init(w, a, share);
+      const uint64_t last_read = ptx::l2_policy_evict_first();
+      int slot = 0;              // ring slot of the next job
+      uint32_t phase = 1;        // parity of its empty barrier to wait for (the first round passes at once)
+      // Waits for the next slot and arms its full barrier.
+      auto take = [&]() -> bool {
+        if (!ptx::mbar_wait(bars.empty(slot), phase, a.status, abort_flag)) return false;
+        if (leader) ptx::mbar_arrive_expect_tx(bars.full(slot), 2 * kSlot);
+        else ptx::mbar_arrive_remote_addr(lf0 + 8 * slot);
+        return true;
+      };
+      auto step = [&]() {
+        if (++slot == kSlots) {
+          slot = 0;
+          phase ^= 1u;
+        }
+      };
+      // The rows of a tile's four 64-token blocks: in the cache, and for P.V
+      // of a tree's last blocks in their copy.
+      struct Rows { int r[4]; };
+      auto look_up = [&](const Piece &p, int t0) {
+        Rows x;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) x.r[t] = block_row<kTree>(a, p, t0 + kSubTok * t, kv_rows);
+        return x;
+      };
+      // V sub-stages of the tile at token t0 of piece p: tokens t0 + 64t..,
+      // latent columns 256g + 128 * rank .. +128, one 3D box: 64 rows x both
+      // 64-column chunks.
+      auto issue_v = [&](const Piece &p, int t0, const Rows &x) -> bool {
+        const int nsub = tile_subs(p, t0);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          if (t >= nsub) break;
+          const int tok0 = t0 + kSubTok * t;
+          const bool copied = kTree && tok0 + kSubTok > p.cached;
+          const CUtensorMap *map = copied ? &mapT : &mapV2;
+          const int y = copied ? p.b * kTreeCopyRows + tok0 - p.cached / kTile * kTile : x.r[t];
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            const int chunk0 = 4 * g + 2 * (int)rank;
+            uint8_t *dst = sRing + slot * kSlot;
+            if (!kTree && tok0 + kSubTok > p.ctx) {
+              // The block runs past the sequence: its load completes on a
+              // barrier of its own, where the helper warp waits, which zeroes
+              // the rows past the end and then arrives for this CTA.
+              if (!ptx::mbar_wait(bars.empty(slot), phase, a.status, abort_flag)) return false;
+              end_slot[g] = slot;
+              ptx::mbar_arrive_expect_tx(bars.end(g), kSlot);
+              ptx::tma_load_3d(dst, map, bars.end(g), 0, y, chunk0);
+            } else {
+              if (!take()) return false;
+              ptx::tma_load_3d_pair_hint(dst, map, lf0 + 8 * slot, 0, y, chunk0, last_read);
             }
-            __syncwarp();
-            continue;
+            step();
           }
-          // The block runs past the sequence: its load completes on a barrier
-          // of this warp's, which zeroes the rows past the end, so that no
-          // unwritten cache row (possibly NaN) reaches P.V, and then arrives
-          // for its CTA without any bytes.
-          if (ptx::elect_one()) {
-            ptx::mbar_arrive_expect_tx(bars.end(pid), kSlot);
-            ptx::tma_load_3d(dst, map, bars.end(pid), 0, y, chunk0);
+        }
+        return true;
+      };
+      Piece pc, vpc;             // vpc, vt0, vx: the tile whose V sub-stages are pending
+      Rows x, vx;
+      int vt0 = 0, npc = 0;
+      bool vpending = false, ok = true;
+      while (ok && walk_next<kTree>(w, a, share, pc)) {
+        if (npc > 0 && !ptx::mbar_wait(bars.qempty(), (npc - 1) & 1, a.status, abort_flag)) break;
+        if (leader) ptx::mbar_arrive_expect_tx(bars.qfull(), 2 * kQBytes);
+        for (int c = 0; c < 9; ++c) {
+          if (kTree)   // rows past the sequence's are zero-filled
+            ptx::tma_load_3d_pair(sQ + c * 8192, &mapQ, lq, 64 * c,
+                                  128 * (pc.v - pc.b * a.tree.groups) + 64 * (int)rank, pc.b);
+          else
+            ptx::tma_load_2d_pair(sQ + c * 8192, &mapQ, lq, 64 * c, pc.b * 128 + 64 * (int)rank);
+        }
+        Rows next = look_up(pc, pc.tok_begin);
+        for (int k = 0; k < pc.ntiles && ok; ++k) {
+          const int t0 = pc.tok_begin + kTileTok * k;
+          x = next;
+          if (k + 1 < pc.ntiles) next = look_up(pc, t0 + kTileTok);
+          // K chunks of this tile: this CTA's 128 tokens x 64 columns each.
+          const int y0 = rank ? x.r[2] : x.r[0], y1 = rank ? x.r[3] : x.r[1];
+#pragma unroll 1
+          for (int c = 0; c < 9; ++c) {
+            if (!take()) { ok = false; break; }
+            uint8_t *dst = sRing + slot * kSlot;
+            if (!boxes64) {
+              ptx::tma_load_2d_pair(dst, &mapK, lf0 + 8 * slot, 64 * c, y0);
+            } else {
+              // 64-token pages or selected blocks: two 64-row boxes.
+              ptx::tma_load_2d_pair(dst, &mapV, lf0 + 8 * slot, 64 * c, y0);
+              ptx::tma_load_2d_pair(dst + 8192, &mapV, lf0 + 8 * slot, 64 * c, y1);
+            }
+            step();
           }
-          __syncwarp();
-          if (!warp_wait(bars.end(pid), nend & 1, a.status, abort_flag)) return false;
-          ++nend;
-          const int row0 = p.ctx - tok0;
-          for (int u = lane; u < (64 - row0) * 16; u += 32)
+          if (!ok) break;
+          if (vpending && !issue_v(vpc, vt0, vx)) { ok = false; break; }
+          vpc = pc;
+          vt0 = t0;
+          vx = x;
+          vpending = true;
+        }
+        ++npc;
+      }
+      if (ok && vpending) issue_v(vpc, vt0, vx);
+    }
+  } else if (warp == kHelperWarp) {
+    // ----------------------------------------- rows behind a sequence's end
+    // Zeroes what the last partial block's load brought from behind the
+    // sequence, so that no unwritten cache row (possibly NaN) reaches P.V.
+    if (!kTree) {
+      const uint32_t lf0 = ptx::leader_addr(bars.full(0));
+      Walk w;
+      walk_init(w, a, share);
+      Piece pc;
+      int n = 0;
+      bool ok = true;
+      while (ok && walk_next<kTree>(w, a, share, pc)) {
+        const int row0 = pc.ctx % kSubTok;
+        if (pc.tok_end != pc.ctx || row0 == 0) continue;
+        for (int g = 0; g < 2; ++g) {
+          if (!warp_wait(bars.end(g), n & 1, a.status, abort_flag)) { ok = false; break; }
+          const int s = end_slot[g];
+          uint8_t *dst = sRing + s * kSlot;
+          for (int u = lane; u < (kSubTok - row0) * 16; u += 32)
             *reinterpret_cast<uint4 *>(dst + (u & 8) * 1024 + (row0 + (u >> 4)) * 128 + (u & 7) * 16) =
                 make_uint4(0, 0, 0, 0);
           ptx::fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive_remote_addr(lf0 + 8 * s);
         }
+        ++n;
       }
-      return true;
-    };
-    while (ok && walk_next<kTree>(w, a, share, pc)) {
-      if (pid == 0) {
-        if (npc > 0 && !warp_wait(bars.qempty(), (npc - 1) & 1, a.status, abort_flag)) break;
-        if (ptx::elect_one()) {
-          if (leader) ptx::mbar_arrive_expect_tx(bars.qfull(), 2 * kQBytes);
-          for (int c = 0; c < 9; ++c) {
-            if (kTree)   // rows past the sequence's are zero-filled
-              ptx::tma_load_3d_pair(sQ + c * 8192, &mapQ, lq, 64 * c,
-                                    128 * (pc.v - pc.b * a.tree.groups) + 64 * (int)rank, pc.b);
-            else
-              ptx::tma_load_2d_pair(sQ + c * 8192, &mapQ, lq, 64 * c, pc.b * 128 + 64 * (int)rank);
-          }
-        }
-        __syncwarp();
-      }
-      for (int k = 0; k < pc.ntiles && ok; ++k) {
-        // K chunks of this tile: this CTA's 128 tokens x 64 columns each.
-        const int t0 = pc.tok_begin + kTileTok * k;
-        const int tr = t0 + kHalfTok * (int)rank;
-        const int y0 = block_row<kTree>(a, pc, tr, kv_rows);
-        const int y1 = boxes64 ? block_row<kTree>(a, pc, tr + kSubTok, kv_rows) : 0;
-        for (int c = 0; c < 9; ++c) {
-          const int s = acquire();
-          if (s == -2) continue;
-          if (s < 0) { ok = false; break; }
-          if (ptx::elect_one()) {
-            uint8_t *dst = sRing + s * kSlot;
-            arm(s);
-            if (!boxes64) {
-              ptx::tma_load_2d_pair(dst, &mapK, lf0 + 8 * s, 64 * c, y0);
-            } else {
-              // 64-token pages or selected blocks: two 64-row boxes.
-              ptx::tma_load_2d_pair(dst, &mapV, lf0 + 8 * s, 64 * c, y0);
-              ptx::tma_load_2d_pair(dst + 8192, &mapV, lf0 + 8 * s, 64 * c, y1);
-            }
-          }
-          __syncwarp();
-        }
-        if (!ok) break;
-        if (vpending && !issue_v(vpc, vt0)) { ok = false; break; }
-        vpc = pc;
-        vt0 = t0;
-        vpending = true;
-      }
-      ++npc;
     }
-    if (ok && vpending) issue_v(vpc, vt0);
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issue
     const bool issuer = ptx::elect_one();
