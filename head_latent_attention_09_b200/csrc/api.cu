@@ -382,11 +382,30 @@ bool tree_tc(const mla_config &c) {
 }
 
 struct TreeShape {
-  int groups, group_rows, parts, tile;
+  int groups, group_rows, gang, runs, parts, tile;
   long long plan_seqs;
   WsLayout L;
   size_t copy_off, total;
 };
+
+// Workers that walk a sequence together, each for one of its groups.  A gang
+// of n reads the cache from HBM once for n groups, but leaves workers idle when
+// n does not divide their number or that of the groups: the cost of a choice is
+// taken as (1 + 0.4 / n) / (share of the workers that have work).
+int tree_gang(int groups, int workers) {
+  int best = 1;
+  double least = 1e30;
+  for (int n = 1; n <= 16 && n <= groups && n <= workers; ++n) {
+    const int runs = (groups + n - 1) / n;
+    const double used = (double)groups / (runs * n) * ((double)(workers / n * n) / workers);
+    const double cost = (1.0 + 0.4 / n) / used;
+    if (cost < least) {
+      least = cost;
+      best = n;
+    }
+  }
+  return best;
+}
 
 TreeShape tree_shape(const mla_handle *h, bool tc, int B, int T, int num_parts) {
   const mla_config &c = h->cfg;
@@ -394,14 +413,17 @@ TreeShape tree_shape(const mla_handle *h, bool tc, int B, int T, int num_parts) 
   const long long rows = (long long)T * c.n_h;
   t.group_rows = tc ? 128 : c.n_h;
   t.groups = (int)ceil_div_ll(rows, t.group_rows);
-  t.parts = num_parts > 0 ? num_parts : (tc ? h->num_sms / 2 : h->num_sms * 4);
+  const int workers = num_parts > 0 ? num_parts : (tc ? h->num_sms / 2 : h->num_sms * 4);
+  t.gang = tc ? tree_gang(t.groups, workers) : 1;
+  t.runs = (t.groups + t.gang - 1) / t.gang;
+  t.parts = workers / t.gang;
   t.tile = tc ? 256 : kTile;
-  t.plan_seqs = (long long)B * t.groups;
+  t.plan_seqs = (long long)B * t.runs;
   if (t.plan_seqs > kMaxPlanSeqs) {
     t.total = 0;
     return t;
   }
-  t.L = tree_ws_layout(t.group_rows, c.d_c, (int)t.plan_seqs, t.parts);
+  t.L = tree_ws_layout(t.group_rows, c.d_c, (int)t.plan_seqs, t.parts, t.gang);
   t.copy_off = t.L.total;
   t.total = align_up(t.L.total + (tc ? tree_copy_bytes(B) : 0), 256);
   return t;
@@ -452,6 +474,8 @@ int mla_tree_attn(mla_handle *h, const void *q_abs, const void *cache, long long
     a.status = h->d_status;
     a.tree.T = T;
     a.tree.groups = t.groups;
+    a.tree.gang = t.gang;
+    a.tree.runs = t.runs;
     a.tree.group_rows = t.group_rows;
     a.tree.seq_rows = T * c.n_h;
     a.tree.mask = tree_mask;
@@ -459,7 +483,7 @@ int mla_tree_attn(mla_handle *h, const void *q_abs, const void *cache, long long
     a.tree.lse = lse;
     a.tree.copy_off = t.copy_off;
     PlanSource src{ctx_len};
-    src.groups = t.groups;
+    src.runs = t.runs;
     src.drafted = T;
     cudaError_t e;
     if (tc) {

@@ -30,7 +30,7 @@ template <> __device__ __forceinline__ __nv_bfloat16 narrow<__nv_bfloat16>(float
 // by HBM for a whole prompt, by the launch for a decode step.
 // ---------------------------------------------------------------------------
 constexpr int kKeyThreads = 288;     // bf16 rows of 576: 72 units x 4 row groups
-constexpr int kKeyBatch = 16;        // rows a thread has in flight
+constexpr int kKeyBatch = 8;         // rows a thread has in flight (x 3 resident blocks: 110 KB an SM)
 
 template <typename T, int V>
 struct alignas(sizeof(T) * V) Unit {
@@ -38,7 +38,7 @@ struct alignas(sizeof(T) * V) Unit {
 };
 
 template <typename T, int V>
-__global__ void __launch_bounds__(kKeyThreads) block_keys_kernel(AttnArgs a, const int *ctx_begin, const int *ctx_len,
+__global__ void __launch_bounds__(kKeyThreads, 3) block_keys_kernel(AttnArgs a, const int *ctx_begin, const int *ctx_len,
                                                                  T *keys, int key_blocks, int D) {
   __shared__ float part[kKeyThreads * V];
   pdl_trigger();
@@ -76,26 +76,30 @@ __global__ void __launch_bounds__(kKeyThreads) block_keys_kernel(AttnArgs a, con
 #pragma unroll
       for (int e = 0; e < V; ++e) acc[e] = 0.f;
       if (g < G && u < units) {
-        for (int r0 = g; r0 < n; r0 += G * kKeyBatch) {
-          Unit<T, V> x[kKeyBatch];
+        if (run && n == kTile && kTile % (G * kKeyBatch) == 0) {
+          const Unit<T, V> *p = cache + (first + g) * units + u;
+          const long long step = (long long)G * units;
+#pragma unroll 1
+          for (int r0 = 0; r0 < kTile; r0 += G * kKeyBatch, p += kKeyBatch * step) {
+            Unit<T, V> x[kKeyBatch];
 #pragma unroll
-          for (int k = 0; k < kKeyBatch; ++k) {
-            const int r = r0 + G * k;
-            if (r >= n) continue;
-            const long long row = run ? first + r : token_row(a, b, j * kTile + r);
-            if (row >= 0) {
-              x[k] = cache[row * units + u];
-            } else {
-              atomicOr(a.status, kStatusBounds);
+            for (int k = 0; k < kKeyBatch; ++k) x[k] = p[k * step];
 #pragma unroll
-              for (int e = 0; e < V; ++e) x[k].e[e] = narrow<T>(0.f);
-            }
+            for (int k = 0; k < kKeyBatch; ++k)
+#pragma unroll
+              for (int e = 0; e < V; ++e) acc[e] += widen<T>(x[k].e[e]);
           }
+        } else {
+#pragma unroll 1
+          for (int r = g; r < n; r += G) {
+            const long long row = run ? first + r : token_row(a, b, j * kTile + r);
+            if (row < 0) {
+              atomicOr(a.status, kStatusBounds);
+              continue;
+            }
+            const Unit<T, V> x = cache[row * units + u];
 #pragma unroll
-          for (int k = 0; k < kKeyBatch; ++k) {
-            if (r0 + G * k >= n) continue;
-#pragma unroll
-            for (int e = 0; e < V; ++e) acc[e] += widen<T>(x[k].e[e]);
+            for (int e = 0; e < V; ++e) acc[e] += widen<T>(x.e[e]);
           }
         }
         if (g > 0) {

@@ -144,13 +144,13 @@ __host__ __device__ inline long long plan_share_of_tile(long long t, long long P
 }
 __host__ __device__ inline long long ceil_div_ll(long long a, long long b) { return (a + b - 1) / b; }
 
-// What the plan cuts into tiles.  A plan sequence is one of `groups` row groups
-// of a batch sequence (1 except for a tree of drafted tokens, whose query rows
-// are cut into groups; plan sequence v belongs to batch sequence v / groups).
+// What the plan cuts into tiles.  A plan sequence is one of `runs` passes over a
+// batch sequence (1 except for a tree of drafted tokens, whose query rows are
+// taken in runs of groups; plan sequence v belongs to batch sequence v / runs).
 struct PlanSource {
   const int *ctx_len;              // [B] cached tokens
   const int *ctx_begin = nullptr;  // [B] first attended token, or NULL (0)
-  int groups = 1;
+  int runs = 1;
   int drafted = 0;                 // tree: drafted tokens behind the ctx_len cached ones
   const int *sel = nullptr;        // selected blocks [B, sel_k], or NULL (every block)
   const int *n_sel = nullptr;      // [B] how many of them
@@ -212,11 +212,11 @@ inline WsLayout ws_layout(const mla_config &cfg, int B, int P) {
 }
 
 // Tree attention: the query rows (drafted token, head) of a sequence are cut
-// into groups of `rows`, each a plan sequence.  Only a group that is split
-// between shares leaves partials, and a share holds at most two such pieces
-// (its first and its last), which take slots 2w and 2w + 1 of the 2 P.
-inline WsLayout tree_ws_layout(int rows, int d_c, int plan_seqs, int P) {
-  return ws_layout_rows(rows, d_c, plan_seqs, P, 2ll * P);
+// into groups of `rows`.  Only a group that is split between shares leaves
+// partials, and each of a share's `gang` workers holds at most two such pieces
+// (its first and its last): 2 P gang slots.
+inline WsLayout tree_ws_layout(int rows, int d_c, int plan_seqs, int P, int gang) {
+  return ws_layout_rows(rows, d_c, plan_seqs, P, 2ll * P * gang);
 }
 
 // The tensor-core kernel reads the blocks that hold drafted tokens, the last
@@ -232,10 +232,14 @@ inline size_t tree_copy_bytes(int batch) { return (size_t)batch * kTreeCopyRows 
 // Tree of drafted tokens: the query rows of sequence b are (t, head), t
 // outermost, T * n_h of them in `groups` groups of `group_rows`; drafted token
 // t sits in cache slot cached + t and attends every cached token and the
-// drafted ones whose bit is set in mask[b, t].
+// drafted ones whose bit is set in mask[b, t].  Groups of a sequence are taken
+// `gang` at a time: a plan sequence is a run of `gang` groups, and a share is
+// worked on by `gang` workers that walk the same tokens at the same time, each
+// for its own group, so that a row comes from HBM once for all of them.
 struct TreeArgs {
   int T = 0;                                // 0: no tree
   int groups = 1, group_rows = 0, seq_rows = 0;
+  int gang = 1, runs = 1;                   // runs = ceil(groups / gang): plan sequences per batch sequence
   const unsigned long long *mask = nullptr; // [batch, T]
   void *out = nullptr;                      // [batch, T, n_h, d_c], the cache's dtype
   float *lse = nullptr;                     // [batch, T, n_h] or NULL
@@ -265,7 +269,7 @@ struct AttnArgs {
   // sequence is then token t % 64 of its block sel[b, t / 64].
   const int *sel = nullptr;
   int sel_k = 0;
-  TreeArgs tree;     // B is then the number of plan sequences (groups x batch)
+  TreeArgs tree;     // B is then the number of plan sequences (runs x batch)
 };
 
 // ---------------------------------------------------------------------------
@@ -327,16 +331,16 @@ __device__ __forceinline__ long long selected_row(const AttnArgs &a, int b, long
 
 // How a piece of tree attention ends.  A group whose tiles all lie in one
 // share is written out at once; a part of a split group leaves a partial in
-// one of its share's two slots.
+// one of its worker's two slots.
 struct TreePiece {
   bool whole;
   long long slot;
 };
-__device__ __forceinline__ TreePiece tree_piece(const long long *tile_prefix, int v, long long w, long long P,
-                                                long long Ttot) {
+__device__ __forceinline__ TreePiece tree_piece(const AttnArgs &a, const long long *tile_prefix, int v, long long w,
+                                                int member, long long P, long long Ttot) {
   const long long s0 = tile_prefix[v], s1 = tile_prefix[v + 1];
   const long long t0 = plan_begin(w, P, Ttot), t1 = plan_begin(w + 1, P, Ttot);
-  return {s0 >= t0 && s1 <= t1, 2 * w + (s0 > t0 ? 1 : 0)};
+  return {s0 >= t0 && s1 <= t1, 2 * (w * a.tree.gang + member) + (s0 > t0 ? 1 : 0)};
 }
 
 cudaError_t launch_attn_simt(const AttnArgs &a, int P, bool fp32, cudaStream_t s);
@@ -345,7 +349,7 @@ cudaError_t launch_tree_attn_simt(const AttnArgs &a, int P, bool fp32, cudaStrea
 cudaError_t launch_combine(const mla_config &cfg, const char *ws, const WsLayout &L, int B,
                            void *ctx_lat, float *lse, cudaStream_t s, bool out_f32 = false);
 // Tree attention: merge of the groups that are split between shares, straight
-// into the outputs (in P x group_rows warps; the other groups are there already).
+// into the outputs (in P x gang x group_rows warps; the others are there already).
 cudaError_t launch_tree_combine(const AttnArgs &a, int P, bool fp32, cudaStream_t s);
 // Accepted path of a drafted tree: row ctx_len[b] + path[b, i] of the cache
 // moves to ctx_len[b] + i, i < n_path[b]; new_len[b] = ctx_len[b] + n_path[b].

@@ -88,7 +88,7 @@ __device__ void make_plan(const PlanSource &src, int B, int P_req, long long cap
   for (int b = b0; b < b1; ++b) {
     // A length outside [0, cap] is flagged and clamped; the tiles below and
     // every attention kernel use the clamped length.
-    const int seq = src.groups > 1 ? b / src.groups : b;
+    const int seq = src.runs > 1 ? b / src.runs : b;
     long long c = src.ctx_len[seq];
     if (c < 0 || c > cap) {
       atomicOr(status, kStatusBounds);
@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(256) attn_simt_kernel(AttnArgs a) {
     }
     if (kTree) {
       // a row that attends nothing is zero; a NaN sum stays NaN
-      const TreePiece tpc = tree_piece(tp, b, w, P, Ttot);
+      const TreePiece tpc = tree_piece(a, tp, b, w, 0, P, Ttot);
       const float inv = l == 0.f ? 0.f : 1.f / l;
       const float z = l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * 0.69314718055994531f;
       const long long orow = (long long)b * a.n_h + h, prow = part_row(a.L, tpc.slot, h);
@@ -632,7 +632,7 @@ cudaError_t launch_plan(const PlanSource &src, int B, int P, long long cap, int 
 }
 
 cudaError_t launch_tree_plan_copy(const PlanSource &src, const AttnArgs &a, int P, long long cap, cudaStream_t s) {
-  const int batch = a.B / src.groups;
+  const int batch = a.B / src.runs;
   if (a.d_c + a.d_r != 576 || src.drafted > kTreeMaxDrafted) return cudaErrorNotSupported;
   const int threads = a.B >= 1024 ? 1024 : (a.B <= 288 ? 288 : (a.B + 31) / 32 * 32);
   return launch_pdl(tree_plan_copy_kernel, dim3(1 + batch * kCopyBlocks), dim3(threads), 0, s, 1, src, a, P, cap);

@@ -105,7 +105,8 @@ constexpr uint32_t kIdescPV = idesc_bf16(128, 256, false, true);
 
 struct Piece {
   int b;               // batch sequence
-  int v;               // plan sequence (b, or a row group of b for a tree)
+  int v;               // plan sequence (b, or a run of row groups of b for a tree)
+  int g;               // tree: the worker's row group of the run
   long long piece;     // global piece index
   int tok_begin;       // first token of the piece in sequence b
   int tok_end;         // one past the last token attended by this piece
@@ -120,6 +121,7 @@ struct Walk {
   long long P, Ttot, t0, t1;
   int b;
   int B;
+  int member;   // tree: which of the share's workers this is
 };
 
 __device__ __forceinline__ void walk_init(Walk &w, const AttnArgs &a, int share) {
@@ -129,6 +131,7 @@ __device__ __forceinline__ void walk_init(Walk &w, const AttnArgs &a, int share)
   w.tp = reinterpret_cast<const long long *>(a.ws + a.L.tile_prefix_off);
   w.pb = reinterpret_cast<const long long *>(a.ws + a.L.piece_base_off);
   w.B = a.B;
+  w.member = (blockIdx.x >> 1) % a.tree.gang;
   if (share >= w.P) {
     w.b = a.B;
     return;
@@ -146,10 +149,12 @@ __device__ __forceinline__ bool walk_next(Walk &w, const AttnArgs &a, int share,
     const long long s0 = w.t0 > w.tp[b] ? w.t0 : w.tp[b];
     const long long s1 = w.t1 < w.tp[b + 1] ? w.t1 : w.tp[b + 1];
     if (s0 >= s1) continue;
+    pc.b = kTree ? b / a.tree.runs : b;
+    pc.v = b;
+    pc.g = kTree ? (b - pc.b * a.tree.runs) * a.tree.gang + w.member : 0;
+    if (kTree && pc.g >= a.tree.groups) continue;
     const int ctx = plan_ctx(a.ws, a.L, b);
     const int beg = kTree ? 0 : plan_begin_tok(a, b);
-    pc.b = kTree ? b / a.tree.groups : b;
-    pc.v = b;
     pc.cached = kTree ? plan_cached(a, b) : ctx;
     pc.piece = w.pb[b] + (share - plan_share_of_tile(w.tp[b], w.P, w.Ttot));
     pc.tok_begin = beg + (int)((s0 - w.tp[b]) * a.plan_tile);
@@ -251,7 +256,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = ptx::cluster_ctarank();
   const bool leader = rank == 0;
-  const int share = blockIdx.x >> 1;
+  const int share = kTree ? (blockIdx.x >> 1) / a.tree.gang : blockIdx.x >> 1;
   pdl_trigger();
 
   if (threadIdx.x == 0) {
@@ -376,7 +381,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int c = 0; c < 9; ++c) {
           if (kTree)   // rows past the sequence's are zero-filled
             ptx::tma_load_3d_pair(sQ + c * 8192, &mapQ, lq, 64 * c,
-                                  128 * (pc.v - pc.b * a.tree.groups) + 64 * (int)rank, pc.b);
+                                  128 * pc.g + 64 * (int)rank, pc.b);
           else
             ptx::tma_load_2d_pair(sQ + c * 8192, &mapQ, lq, 64 * c, pc.b * 128 + 64 * (int)rank);
         }
@@ -554,7 +559,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     while (ok && walk_next<kTree>(w, a, share, pc)) {
       float m_run = -CUDART_INF_F, l_part = 0.f;
       // tree: this thread's query row of the sequence, and its drafted tokens
-      const int row = 128 * (pc.v - pc.b * a.tree.groups) + 64 * (int)rank + h;
+      const int row = 128 * pc.g + 64 * (int)rank + h;
       unsigned long long bits = 0ull;
       if (kTree && row < a.tree.seq_rows) {
         bits = a.tree.mask[(long long)pc.b * a.tree.T + row / a.n_h];
@@ -668,7 +673,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       long long slot = pc.piece;
       bool whole = false;
       if (kTree) {
-        const TreePiece t = tree_piece(w.tp, pc.v, share, w.P, w.Ttot);
+        const TreePiece t = tree_piece(a, w.tp, pc.v, share, w.member, w.P, w.Ttot);
         whole = t.whole;
         slot = t.slot;
       }
@@ -687,7 +692,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int r0 = 64 * (int)rank + (q & 1) * 32;   // first head / row of the warp within the 128
       if (kTree && whole) {
         __nv_bfloat16 *out = reinterpret_cast<__nv_bfloat16 *>(a.tree.out);
-        const int g0 = 128 * (pc.v - pc.b * a.tree.groups) + r0;
+        const int g0 = 128 * pc.g + r0;
 #pragma unroll 1
         for (int c = 0; c < 2; ++c) {
           float v[64];
@@ -759,7 +764,7 @@ template <bool kTree>
 cudaError_t launch_pair(const AttnArgs &a, int P, cudaStream_t s, const std::function<cudaError_t()> *before) {
   if (a.d_c != 512 || a.d_r != 64) return cudaErrorNotSupported;
   if (a.page_size != 0 && a.page_size != kTile) return cudaErrorNotSupported;
-  const int batch = kTree ? a.B / a.tree.groups : a.B;
+  const int batch = kTree ? a.B / a.tree.runs : a.B;
   const long long rows = a.page_size ? a.cache_len * kTile : (long long)batch * a.cache_len;
   if (rows <= 0 || rows >= (1ll << 31) - 256) return cudaErrorNotSupported;
   CUtensorMap mq, mk, mv, mv2, mt;
@@ -791,7 +796,7 @@ cudaError_t launch_pair(const AttnArgs &a, int P, cudaStream_t s, const std::fun
   });
   if (e == cudaSuccess && before) e = (*before)();
   if (e != cudaSuccess) return e;
-  return launch_pdl(attn_pair_kernel<kTree>, dim3(2 * P), dim3(kThreads), kSmemAlloc, s, 1, mq, mk, mv, mv2, mt, a,
+  return launch_pdl(attn_pair_kernel<kTree>, dim3(2 * P * a.tree.gang), dim3(kThreads), kSmemAlloc, s, 1, mq, mk, mv, mv2, mt, a,
                     rows);
 }
 }  // namespace

@@ -12,11 +12,11 @@ template <> __device__ __forceinline__ float cast<float>(float x) { return x; }
 template <> __device__ __forceinline__ __nv_bfloat16 cast<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
 
 // Log-sum-exp merge of the groups that are split between shares.  A share
-// boundary cuts at most one group, so block x takes the group that begins in
-// share x and runs on into share x + 1 (if there is one); y counts blocks of 8
-// query rows, one warp each.  Groups that lie in one share were written by the
-// attention kernel, so the traffic is that of at most 2 P pieces however many
-// groups there are.
+// boundary cuts at most one plan sequence (gang groups), so block x takes
+// member x % gang of the one that begins in share x / gang and runs on into
+// the next (if there is one); y counts blocks of 8 query rows, one warp each.
+// Groups that lie in one share were written by the attention kernel, so the
+// traffic is that of at most 2 P gang pieces however many groups there are.
 template <typename T>
 __global__ void __launch_bounds__(256) tree_combine_kernel(AttnArgs a) {
   pdl_trigger();
@@ -29,7 +29,7 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(AttnArgs a) {
   T *out = reinterpret_cast<T *>(a.tree.out);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (Ttot == 0) {   // a cache without room for a single token: no row attends anything
-    const long long rows = (long long)(a.B / a.tree.groups) * a.tree.seq_rows;
+    const long long rows = (long long)(a.B / a.tree.runs) * a.tree.seq_rows;
     const long long n = (long long)gridDim.x * gridDim.y * 8;
     for (long long r = ((long long)blockIdx.y * gridDim.x + blockIdx.x) * 8 + warp; r < rows; r += n) {
       for (int f = lane; f < a.d_c; f += 32) out[r * a.d_c + f] = cast<T>(0.f);
@@ -37,18 +37,20 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(AttnArgs a) {
     }
     return;
   }
-  const long long w0 = blockIdx.x;
+  const long long w0 = blockIdx.x / a.tree.gang;
+  const int member = blockIdx.x % a.tree.gang;
   if (w0 + 1 >= P) return;
   // the group that holds the first tile of the next share
   const int v = reinterpret_cast<const int *>(a.ws + a.L.share_first_off)[w0 + 1];
   const long long s0 = tp[v], s1 = tp[v + 1];
   if (s0 >= plan_begin(w0 + 1, P, Ttot) || s0 < plan_begin(w0, P, Ttot)) return;   // begins elsewhere
   const int r = blockIdx.y * 8 + warp;
-  const int b = v / a.tree.groups, row = (v - b * a.tree.groups) * a.tree.group_rows + r;
+  const int b = v / a.tree.runs, g = (v - b * a.tree.runs) * a.tree.gang + member;
+  const int row = g * a.tree.group_rows + r;   // past the sequence's rows where there is no group g
   if (r >= a.tree.group_rows || row >= a.tree.seq_rows) return;
   const long long w1 = plan_share_of_tile(s1 - 1, P, Ttot);
   // partials: the last piece of share w0 (or its only one), the first of the others
-  auto part = [&](long long w) { return part_row(a.L, 2 * w + (s0 > plan_begin(w, P, Ttot) ? 1 : 0), r); };
+  auto part = [&](long long w) { return part_row(a.L, tree_piece(a, tp, v, w, member, P, Ttot).slot, r); };
   float m = -CUDART_INF_F;
   for (long long w = w0 + lane; w <= w1; w += 32) m = fmaxf(m, lse[part(w)]);
 #pragma unroll
@@ -140,7 +142,7 @@ cudaError_t accept_units(int row_bytes, void *cache, const AttnArgs &a, const in
 }  // namespace
 
 cudaError_t launch_tree_combine(const AttnArgs &a, int P, bool fp32, cudaStream_t s) {
-  const dim3 grid(P, (a.tree.group_rows + 7) / 8);
+  const dim3 grid(P * a.tree.gang, (a.tree.group_rows + 7) / 8);
   if (grid.y > 65535) return cudaErrorNotSupported;
   return fp32 ? launch_pdl(tree_combine_kernel<float>, grid, dim3(256), 0, s, 1, a)
               : launch_pdl(tree_combine_kernel<__nv_bfloat16>, grid, dim3(256), 0, s, 1, a);
