@@ -125,19 +125,29 @@ def load(path: str | None = None) -> ctypes.CDLL:
 def _ptr(x):
     if x is None:
         return None
+    try:
+        return x.data_ptr()
+    except AttributeError:
+        pass
     if isinstance(x, int):
         return x
-    if hasattr(x, "data_ptr"):
-        return x.data_ptr()
     if isinstance(x, ctypes.c_void_p):
         return x.value
     raise TypeError(f"cannot pass {type(x).__name__} as a pointer")
 
 
+_current_stream = None      # torch.cuda.current_stream, once a GPU has been seen
+
+
 def _stream(s):
     if s is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream if torch.cuda.is_available() else None
+        global _current_stream
+        if _current_stream is None:
+            import torch
+            if not torch.cuda.is_available():
+                return None
+            _current_stream = torch.cuda.current_stream
+        return _current_stream().cuda_stream
     if isinstance(s, int):
         return s
     return s.cuda_stream

@@ -547,12 +547,12 @@ int mla_block_scores(mla_handle *h, const void *q_abs, const void *keys, int key
   const bool tc = h->cfg.dtype == MLA_BF16 && h->cfg.d_c == 512 && h->cfg.d_r == 64;
   cudaError_t e = cudaErrorNotSupported;
   if (tc)
-    e = launch_block_scores(h->cfg, true, scale_log2_of(h), q_abs, keys, key_blocks, ctx_len, B, scores,
-                            (char *)workspace, L, h->d_status, (cudaStream_t)stream);
+    e = launch_block_scores_tc(h->cfg, scale_log2_of(h), q_abs, keys, key_blocks, ctx_len, B, scores, h->d_status,
+                               (cudaStream_t)stream);
   if (strict_refuses(h, tc, e)) return MLA_ERR_UNSUPPORTED;
   if (e == cudaErrorNotSupported)
-    e = launch_block_scores(h->cfg, false, scale_log2_of(h), q_abs, keys, key_blocks, ctx_len, B, scores,
-                            (char *)workspace, L, h->d_status, (cudaStream_t)stream);
+    e = launch_block_scores_simt(h->cfg, scale_log2_of(h), q_abs, keys, key_blocks, ctx_len, B, scores,
+                                 (char *)workspace, L, h->d_status, (cudaStream_t)stream);
   return e == cudaErrorNotSupported ? MLA_ERR_UNSUPPORTED : from_cuda(e);
 }
 

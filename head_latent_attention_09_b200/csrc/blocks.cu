@@ -91,15 +91,24 @@ __global__ void __launch_bounds__(kKeyThreads, 3) block_keys_kernel(AttnArgs a, 
           }
         } else {
 #pragma unroll 1
-          for (int r = g; r < n; r += G) {
-            const long long row = run ? first + r : token_row(a, b, j * kTile + r);
-            if (row < 0) {
-              atomicOr(a.status, kStatusBounds);
-              continue;
-            }
-            const Unit<T, V> x = cache[row * units + u];
+          for (int r0 = g; r0 < n; r0 += G * kKeyBatch) {
+            Unit<T, V> x[kKeyBatch];
 #pragma unroll
-            for (int e = 0; e < V; ++e) acc[e] += widen<T>(x.e[e]);
+            for (int k = 0; k < kKeyBatch; ++k) {
+              const int r = r0 + G * k;
+              const long long row = r >= n ? -1 : (run ? first + r : token_row(a, b, j * kTile + r));
+              if (row >= 0) {
+                x[k] = cache[row * units + u];
+              } else {
+                if (r < n) atomicOr(a.status, kStatusBounds);
+#pragma unroll
+                for (int e = 0; e < V; ++e) x[k].e[e] = narrow<T>(0.f);
+              }
+            }
+#pragma unroll
+            for (int k = 0; k < kKeyBatch; ++k)
+#pragma unroll
+              for (int e = 0; e < V; ++e) acc[e] += widen<T>(x[k].e[e]);
           }
         }
         if (g > 0) {
@@ -132,8 +141,8 @@ cudaError_t launch_keys(const AttnArgs &a, const int *ctx_begin, const int *ctx_
 }
 
 // ---------------------------------------------------------------------------
-// scores, first half: x (in log2 units) of a tile of 128 blocks against the
-// heads, and per head the tile's maximum and sum of 2^(x - maximum).
+// scores: x (in log2 units) of a tile of 128 blocks against the heads, per head
+// the tile's maximum and sum of 2^(x - maximum), and from these the shares.
 // ---------------------------------------------------------------------------
 constexpr int kScoreTile = 128;
 
@@ -144,7 +153,8 @@ __device__ __forceinline__ float log2_tokens(int j, int ctx) {
   return n >= kTile ? 6.f : log2f((float)n);
 }
 
-// CUDA cores: one warp per head, the query row in registers.
+// CUDA cores, two launches: first x and the statistics, one warp per head, the
+// query row in registers (also bf16 beyond the tensor-core kernel's 4096 blocks).
 template <typename T>
 __global__ void __launch_bounds__(256) score_logits_simt_kernel(const T *q_abs, const T *keys, int key_blocks,
                                                                 const int *ctx_len, int n_h, int D, float scale_log2,
@@ -182,31 +192,38 @@ __global__ void __launch_bounds__(256) score_logits_simt_kernel(const T *q_abs, 
   if (lane == 0) stats[((long long)b * L.tiles + tile) * L.head_rows + h] = make_float2(m, sum);
 }
 
-// Tensor cores (rows of 576 bf16): S = Q K^T with the heads as M (128, zero
-// filled) and the tile's 128 blocks as N, so that a thread owns one head's row
-// of the accumulator and its statistics need no exchange.  Nine 64-column
-// chunks of both operands stream through a ring of six 32 KB stages.  At one
-// to a few tiles per sequence the time is that of one load-multiply-store
-// chain; the means are 1/64 of the cache's bytes.
+// Tensor cores (rows of 576 bf16), both halves in one launch: a cluster of up
+// to eight CTAs per sequence, each with up to four tiles of 128 blocks.
+//   S = Q K^T  M = 128 heads (zero filled), N = 128 blocks a tile; nine
+//              64-column chunks of Q and of the tiles' rows stream through a
+//              ring of stages.
+// A thread owns one head's row of the accumulator, so its maximum and sum need
+// no exchange within the CTA; the cluster's CTAs exchange them through
+// distributed shared memory, and the shares are then added over the heads by a
+// transposing reduction (31 shuffles for 32 columns).  The logits never leave
+// tensor memory.  The rows are 1/64 of the cache's bytes: the time is one chain
+// of load, multiply and three passes over tensor memory.
 constexpr int kSThreads = 192;
-constexpr int kSStages = 6;
-constexpr int kSStage = 32768;
-constexpr int kSSmem = kSStages * kSStage + 1024;
+constexpr int kSMaxTiles = 4, kSMaxCluster = 8;
+constexpr int kSRing = 6 * 32768;      // bytes of stages: 6, 4, 3 or 2 of (1 + tiles) 16 KB chunks
+constexpr int kSSmem = kSRing + 1024;
 
 __global__ void __launch_bounds__(kSThreads, 1)
-    score_logits_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
-                           int key_blocks, const int *ctx_len, int n_h, float scale_log2, float *logits, float2 *stats,
-                           ScoreLayout L, unsigned *status) {
+    score_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK, int key_blocks,
+                    const int *ctx_len, int n_h, float scale_log2, float *scores, int tiles_per_cta, int stages,
+                    uint32_t tmem_cols, unsigned *status) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  __shared__ uint64_t full[kSStages], empty[kSStages], done;
+  __shared__ uint64_t full[6], empty[6], done;
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int abort_flag;
+  __shared__ float2 stat[2][128];                         // per head: maximum and sum over this CTA's blocks
+  __shared__ float part[4][kSMaxTiles * kScoreTile];      // per epilogue warp: shares summed over its 32 heads
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int tile = blockIdx.x, h0 = blockIdx.y * 128, b = blockIdx.z;
+  const int rank = blockIdx.x, b = blockIdx.y;
   pdl_trigger();
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kSStages; ++i) {
+    for (int i = 0; i < 6; ++i) {
       ptx::mbar_init(&full[i], 1);
       ptx::mbar_init(&empty[i], 1);
     }
@@ -215,7 +232,7 @@ __global__ void __launch_bounds__(kSThreads, 1)
     ptx::fence_barrier_init();
   }
   if (warp == 1) {
-    ptx::tmem_alloc(&tmem_slot, 128);
+    ptx::tmem_alloc(&tmem_slot, tmem_cols);
     ptx::tmem_relinquish();
   }
   ptx::tc_fence_before();
@@ -223,80 +240,148 @@ __global__ void __launch_bounds__(kSThreads, 1)
   ptx::tc_fence_after();
   const uint32_t tmem = tmem_slot;
   pdl_wait();
-  const int ctx = ctx_len[b], nb = min(blocks_of(ctx), key_blocks);
-  const bool work = tile * kScoreTile < nb;
-  if (warp == 0) {
-    if (work && ptx::elect_one()) {
-      ptx::tma_prefetch_desc(&mapQ);
-      ptx::tma_prefetch_desc(&mapK);
-      for (int c = 0; c < 9; ++c) {
-        const int s = c % kSStages;
-        if (c >= kSStages && !ptx::mbar_wait(&empty[s], 0, status, &abort_flag)) break;
-        ptx::mbar_arrive_expect_tx(&full[s], kSStage);
-        ptx::tma_load_3d(sm + s * kSStage, &mapQ, &full[s], 64 * c, h0, b);
-        ptx::tma_load_3d(sm + s * kSStage + 16384, &mapK, &full[s], 64 * c, tile * kScoreTile, b);
+  const int ctx = ctx_len[b], all = blocks_of(ctx), nb = min(all, key_blocks);
+  if ((all > key_blocks || ctx < 0) && rank == 0 && threadIdx.x == 0) atomicOr(status, kStatusBounds);
+  const int j0 = rank * tiles_per_cta * kScoreTile;       // first block of this CTA
+  const int own = min(max((nb - j0 + kScoreTile - 1) / kScoreTile, 0), tiles_per_cta);   // its tiles that hold blocks
+  const int stage = (1 + tiles_per_cta) * 16384;
+  const int head_tiles = (n_h + 127) / 128;
+  const int q = warp & 3;
+  const bool epi = warp >= 2;
+  float acc[kSMaxTiles] = {0.f, 0.f, 0.f, 0.f};           // thread t of the epilogue: block t of each tile
+  // Columns [64 g, 64 g + 64) of this thread's row of tile t, in log2 units.
+  auto row64 = [&](int t, int g, float (&v)[64]) {
+    ptx::tmem_ld64_sync(tmem + ((uint32_t)(q * 32) << 16) + t * kScoreTile + 64 * g, reinterpret_cast<uint32_t *>(v));
+    const int jb = j0 + t * kScoreTile + 64 * g;
+    const float last = log2_tokens(nb - 1, ctx);
+#pragma unroll
+    for (int j = 0; j < 64; ++j)
+      v[j] = jb + j < nb ? fmaf(v[j], scale_log2, jb + j == nb - 1 ? last : 6.f) : -CUDART_INF_F;
+  };
+  for (int ht = 0; ht < head_tiles; ++ht) {
+    if (warp == 0) {
+      if (own > 0 && ptx::elect_one()) {
+        for (int c = 0; c < 9; ++c) {
+          const int it = ht * 9 + c, s = it % stages;
+          if (it >= stages && !ptx::mbar_wait(&empty[s], (it / stages - 1) & 1, status, &abort_flag)) break;
+          uint8_t *at = sm + s * stage;
+          ptx::mbar_arrive_expect_tx(&full[s], (1 + own) * 16384);
+          ptx::tma_load_3d(at, &mapQ, &full[s], 64 * c, ht * 128, b);
+          for (int t = 0; t < own; ++t)
+            ptx::tma_load_3d(at + (1 + t) * 16384, &mapK, &full[s], 64 * c, j0 + t * kScoreTile, b);
+        }
       }
-    }
-  } else if (warp == 1) {
-    if (work && ptx::elect_one()) {
-      constexpr uint32_t id = idesc_bf16(128, kScoreTile, false, false);
-      bool ok = true;
-      for (int c = 0; c < 9 && ok; ++c) {
-        const int s = c % kSStages;
-        ok = ptx::mbar_wait(&full[s], c / kSStages, status, &abort_flag);
-        if (!ok) break;
+    } else if (warp == 1) {
+      if (own > 0 && ptx::elect_one()) {
+        constexpr uint32_t id = idesc_bf16(128, kScoreTile, false, false);
+        bool ok = true;
+        for (int c = 0; c < 9 && ok; ++c) {
+          const int it = ht * 9 + c, s = it % stages;
+          ok = ptx::mbar_wait(&full[s], (it / stages) & 1, status, &abort_flag);
+          if (!ok) break;
+          ptx::tc_fence_after();
+          const uint32_t at = ptx::smem_u32(sm + s * stage);
+          for (int t = 0; t < own; ++t)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              ptx::mma_bf16_ss(tmem + t * kScoreTile, ptx::sdesc(at + 32 * k, 16, 1024, 2),
+                               ptx::sdesc(at + (1 + t) * 16384 + 32 * k, 16, 1024, 2), id, (c | k) != 0 ? 1u : 0u);
+          ptx::mma_commit(&empty[s]);
+        }
+        if (ok) ptx::mma_commit(&done);
+      }
+    } else {
+      const int h = ht * 128 + 32 * q + lane;
+      float m = -CUDART_INF_F, sum = 0.f;
+      bool ok = own > 0;
+      if (ok && lane == 0) ok = ptx::mbar_wait(&done, ht & 1, status, &abort_flag);
+      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+      if (ok && lane != 0) ptx::mbar_test_wait(&done, ht & 1);
+      __syncwarp();
+      if (ok && ht * 128 + 32 * q < n_h) {
         ptx::tc_fence_after();
-        const uint32_t at = ptx::smem_u32(sm + s * kSStage);
+        for (int t = 0; t < own; ++t)
+#pragma unroll 1
+          for (int g = 0; g < 2; ++g) {
+            float v[64];
+            row64(t, g, v);
+            float mx[4] = {m, m, m, m};
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          ptx::mma_bf16_ss(tmem, ptx::sdesc(at + 32 * k, 16, 1024, 2), ptx::sdesc(at + 16384 + 32 * k, 16, 1024, 2),
-                           id, (c | k) != 0 ? 1u : 0u);
-        ptx::mma_commit(&empty[s]);
+            for (int j = 0; j < 64; ++j) mx[j & 3] = fmaxf(mx[j & 3], v[j]);
+            const float m2 = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            if (m2 == -CUDART_INF_F) continue;             // no block of the sequence among them
+            float s4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int j = 0; j < 64; ++j) s4[j & 3] += ptx::exp2_approx(v[j] - m2);
+            sum = sum * exp2f(m - m2) + ((s4[0] + s4[1]) + (s4[2] + s4[3]));
+            m = m2;
+          }
       }
-      if (ok) ptx::mma_commit(&done);
+      stat[ht & 1][32 * q + lane] = h < n_h ? make_float2(m, sum) : make_float2(-CUDART_INF_F, 0.f);
     }
-  } else if (work) {
-    const int q = warp & 3, h = h0 + 32 * q + lane;
-    bool ok = true;
-    if (lane == 0) ok = ptx::mbar_wait(&done, 0, status, &abort_flag);
-    ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-    if (ok && lane != 0) ptx::mbar_test_wait(&done, 0);
     __syncwarp();
-    if (ok && h0 + 32 * q < n_h) {
-      ptx::tc_fence_after();
-      float v[kScoreTile];
-      const uint32_t at = tmem + ((uint32_t)(q * 32) << 16);
-      ptx::tmem_ld64_sync(at, reinterpret_cast<uint32_t *>(v));
-      ptx::tmem_ld64_sync(at + 64, reinterpret_cast<uint32_t *>(v) + 64);
-      const int j0 = tile * kScoreTile;
-      float mx[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
-      const float last = log2_tokens(nb - 1, ctx);
+    ptx::cluster_sync_all();
+    if (epi) {
+      if (own > 0 && ht * 128 + 32 * q < n_h) {
+        // the head's log-sum-exp over the sequence's blocks
+        const int h = 32 * q + lane;
+        const uint32_t mine = ptx::smem_u32(&stat[ht & 1][h]);
+        float m = -CUDART_INF_F, sum = 0.f;
+        const int nc = (int)ptx::cluster_nctarank();
+        for (int p = 0; p < nc; ++p) {
+          const float2 s = ptx::ld_shared_cluster_v2f(ptx::mapa_peer(mine, (uint32_t)p));
+          if (s.x == -CUDART_INF_F) continue;
+          const float m2 = fmaxf(m, s.x);
+          sum = sum * exp2f(m - m2) + s.y * exp2f(s.x - m2);
+          m = m2;
+        }
+        const bool real = ht * 128 + h < n_h;
+        const float lse = real ? m + log2f(sum) : 0.f;
+        for (int t = 0; t < own; ++t)
+#pragma unroll 1
+          for (int g = 0; g < 2; ++g) {
+            float v[64];
+            row64(t, g, v);
 #pragma unroll
-      for (int j = 0; j < kScoreTile; ++j) {
-        const int jj = j0 + j;
-        v[j] = jj < nb ? fmaf(v[j], scale_log2, jj == nb - 1 ? last : 6.f) : -CUDART_INF_F;
-        mx[j & 3] = fmaxf(mx[j & 3], v[j]);
-      }
-      const float m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-      float *out = logits + ((long long)b * L.tiles * kScoreTile + j0) * L.head_rows + h;
-      float sm4[4] = {0.f, 0.f, 0.f, 0.f};
+            for (int j = 0; j < 64; ++j) v[j] = real ? ptx::exp2_approx(v[j] - lse) : 0.f;
+            // Sums over the 32 lanes: halving the columns a lane is in charge
+            // of with every exchange leaves lane l columns l and 32 + l.
 #pragma unroll
-      for (int j = 0; j < kScoreTile; ++j) {
-        sm4[j & 3] += ptx::exp2_approx(v[j] - m);
-        if (j0 + j < nb) out[(long long)j * L.head_rows] = v[j];
+            for (int o = 16; o > 0; o >>= 1) {
+              const bool up = (lane & o) != 0;
+#pragma unroll
+              for (int hlf = 0; hlf < 2; ++hlf)
+#pragma unroll
+                for (int j = 0; j < o; ++j) {
+                  float *w = v + 32 * hlf;
+                  const float give = up ? w[j] : w[j + o], keep = up ? w[j + o] : w[j];
+                  w[j] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+                }
+            }
+            part[q][t * kScoreTile + 64 * g + lane] = v[0];
+            part[q][t * kScoreTile + 64 * g + 32 + lane] = v[32];
+          }
       }
-      stats[((long long)b * L.tiles + tile) * L.head_rows + h] = make_float2(m, (sm4[0] + sm4[1]) + (sm4[2] + sm4[3]));
+      ptx::named_bar_sync(1, 128);
+      const int warps = min(4, (n_h - ht * 128 + 31) / 32);    // epilogue warps that hold heads
+      for (int t = 0; t < own; ++t)
+        for (int w = 0; w < warps; ++w) acc[t] += part[w][t * kScoreTile + 32 * q + lane];
     }
-  }
-  ptx::tc_fence_before();
-  __syncthreads();
-  if (warp == 1) {
+    ptx::tc_fence_before();
+    __syncthreads();   // the next heads' MMAs overwrite the accumulator, their sums `part`
     ptx::tc_fence_after();
-    ptx::tmem_dealloc(tmem, 128);
   }
+  if (epi)
+    for (int t = 0; t < tiles_per_cta; ++t) {
+      const int j = j0 + t * kScoreTile + 32 * q + lane;
+      if (j < key_blocks) scores[(long long)b * key_blocks + j] = j < nb ? acc[t] : 0.f;
+    }
+  __syncwarp();
+  if (warp == 1) ptx::tmem_dealloc(tmem, tmem_cols);
+  ptx::cluster_sync_all();   // no CTA leaves while others still read its statistics
 }
 
-// Second half: score_j = sum over heads of 2^(x - lse of the head), one warp
+// Second launch: score_j = sum over heads of 2^(x - lse of the head), one warp
 // per block, the heads across the lanes; blocks the sequence lacks score 0.
 constexpr int kSumBlocks = 64;
 __global__ void __launch_bounds__(256) score_sum_kernel(const float *logits, const float2 *stats, ScoreLayout L,
@@ -338,15 +423,19 @@ __global__ void __launch_bounds__(256) score_sum_kernel(const float *logits, con
 
 // ---------------------------------------------------------------------------
 // selection: the k best blocks of a sequence in rising order.  One block of
-// threads per sequence, the scores in shared memory as unsigned integers of
-// the same order.  The k-th largest is found two bits at a time (16 rounds of
-// three counts, no atomics on shared bins, whose order would not matter but
-// whose collisions would: softmax masses share their leading bits), then one
-// scan over the threads' runs of blocks places the winners.  The order is
-// total (value, then the lower index), so the result is the same however the
-// threads run.
+// threads per sequence; the scores become unsigned integers of the same order,
+// thread t holding a run of consecutive ones (in registers up to 4096 blocks,
+// in shared memory beyond).  The k-th largest is found two bits a round: three
+// counts per thread, summed within the warps by redux and across them through
+// one shared-memory line, so a round is one barrier and no atomics (softmax
+// masses share their leading bits: bins would collide).  The rounds end once
+// a bound leaves exactly k.  One scan over the threads then places the
+// winners.  The order is total (value, then the lower index), so the result
+// is the same however the threads run.  The work is a few KB a sequence: the
+// time is the launch, two dependent reads and the rounds' barriers.
 // ---------------------------------------------------------------------------
 constexpr int kSelMaxBlocks = 49152;   // 192 KB of keys
+constexpr int kSelRegs = 4;            // keys a thread holds in registers
 
 __device__ __forceinline__ uint32_t order_key(float x) {
   if (x != x) return 0u;                     // NaN ranks below everything
@@ -354,20 +443,26 @@ __device__ __forceinline__ uint32_t order_key(float x) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
+template <bool kReg>
 __global__ void __launch_bounds__(1024) block_select_kernel(const float *scores, int n_blocks, const int *ctx_len,
                                                             int k, int n_first, int n_last, int *sel, int *n_sel,
                                                             unsigned *status) {
-  extern __shared__ uint32_t key[];
-  __shared__ int cnt[16][3];
-  __shared__ int wsum[32][2];
+  extern __shared__ uint32_t skey[];
+  __shared__ uint32_t cnt[2][32][2];
   pdl_trigger();
   pdl_wait();
-  const int b = blockIdx.x, tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5;
+  const int b = blockIdx.x, tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5, nw = nt >> 5;
+  const float *x = scores + (long long)b * n_blocks;
+  const int per = kReg ? kSelRegs : (n_blocks + nt - 1) / nt;
+  const int i0 = tid * per;                                // this thread's run of blocks
+  float xr[kSelRegs];
+  if (kReg) {
+#pragma unroll
+    for (int e = 0; e < kSelRegs; ++e) xr[e] = i0 + e < n_blocks ? x[i0 + e] : 0.f;
+  }
   const int all = blocks_of(ctx_len[b]);
   const int n = min(all, n_blocks);
   if (tid == 0 && (all > n_blocks || ctx_len[b] < 0)) atomicOr(status, kStatusBounds);
-  if (tid < 48) cnt[tid / 3][tid % 3] = 0;
-  if (nt < 48 && tid < 16) cnt[(tid + 32) / 3][(tid + 32) % 3] = 0;
   int *out = sel + (long long)b * k;
   const int take = min(n, k);
   for (int i = take + tid; i < k; i += nt) out[i] = -1;
@@ -376,61 +471,86 @@ __global__ void __launch_bounds__(1024) block_select_kernel(const float *scores,
     for (int i = tid; i < n; i += nt) out[i] = i;
     return;
   }
-  const float *x = scores + (long long)b * n_blocks;
-  for (int i = tid; i < n; i += nt) key[i] = i < n_first || i >= n - n_last ? 0xffffffffu : order_key(x[i]);
-  __syncthreads();
-  uint32_t v = 0;   // largest value with at least `take` keys >= it
+  auto key_of = [&](int i, float v) { return i < n_first || i >= n - n_last ? 0xffffffffu : order_key(v); };
+  uint32_t key[kSelRegs];
+  const int i1 = min(n, i0 + per);
+  if (kReg) {
+#pragma unroll
+    for (int e = 0; e < kSelRegs; ++e) key[e] = key_of(i0 + e, xr[e]);
+  } else {
+    for (int i = tid; i < n; i += nt) skey[i] = key_of(i, x[i]);
+    __syncthreads();
+  }
+  // f(key) for each block of this thread's run, in order
+  auto each = [&](auto f) {
+    if (kReg) {
+#pragma unroll
+      for (int e = 0; e < kSelRegs; ++e)
+        if (i0 + e < n) f(i0 + e, key[e]);
+    } else {
+      for (int i = i0; i < i1; ++i) f(i, skey[i]);
+    }
+  };
+  // Sum over the block of two counts below 2^16 in one word, and of another.
+  auto total = [&](int buf, uint32_t a, uint32_t c, uint32_t &sa, uint32_t &sc) {
+    a = __reduce_add_sync(0xffffffffu, a);
+    c = __reduce_add_sync(0xffffffffu, c);
+    if (nw > 1) {
+      if (lane == 0) {
+        cnt[buf][warp][0] = a;
+        cnt[buf][warp][1] = c;
+      }
+      __syncthreads();
+      a = __reduce_add_sync(0xffffffffu, lane < nw ? cnt[buf][lane][0] : 0u);
+      c = __reduce_add_sync(0xffffffffu, lane < nw ? cnt[buf][lane][1] : 0u);
+    }
+    sa = a;
+    sc = c;
+  };
+  uint32_t v = 0;   // largest value found so far with at least `take` keys >= it
 #pragma unroll 1
   for (int r = 0; r < 16; ++r) {
     const uint32_t bit = 1u << (30 - 2 * r);
-    int c1 = 0, c2 = 0, c3 = 0;
-    for (int i = tid; i < n; i += nt) {
-      const uint32_t kk = key[i];
-      c1 += kk >= v + bit;
-      c2 += kk >= v + 2 * bit;
-      c3 += kk >= v + 3 * bit;
-    }
-    c1 = __reduce_add_sync(0xffffffffu, c1);
-    c2 = __reduce_add_sync(0xffffffffu, c2);
-    c3 = __reduce_add_sync(0xffffffffu, c3);
-    if (lane < 3) atomicAdd(&cnt[r][lane], lane == 0 ? c1 : (lane == 1 ? c2 : c3));
-    __syncthreads();
-    v += cnt[r][2] >= take ? 3 * bit : (cnt[r][1] >= take ? 2 * bit : (cnt[r][0] >= take ? bit : 0u));
+    uint32_t c12 = 0, c3 = 0, s12, s3;
+    each([&](int, uint32_t kk) {
+      c12 += (kk >= v + bit ? 1u : 0u) + (kk >= v + 2 * bit ? 0x10000u : 0u);
+      c3 += kk >= v + 3 * bit ? 1u : 0u;
+    });
+    total(r & 1, c12, c3, s12, s3);
+    const int t1 = s12 & 0xffffu, t2 = s12 >> 16, t3 = s3;
+    const int step = t3 >= take ? 3 : (t2 >= take ? 2 : (t1 >= take ? 1 : 0));
+    v += step * bit;
+    if ((step == 3 ? t3 : (step == 2 ? t2 : t1)) == take && step > 0) break;   // exactly the winners are >= v
   }
-  // Thread t places its run of consecutive blocks: those above v, and the
-  // first of those equal to it.
-  const int per = (n + nt - 1) / nt, i0 = min(n, tid * per), i1 = min(n, i0 + per);
+  // Thread t places those of its run above v, and the first of those equal to
+  // it as far as the k-th place reaches.
   int gt = 0, eq = 0;
-  for (int i = i0; i < i1; ++i) {
-    gt += key[i] > v;
-    eq += key[i] == v;
-  }
-  int g = gt, e = eq;   // inclusive prefix over the lanes
+  each([&](int, uint32_t kk) {
+    gt += kk > v;
+    eq += kk == v;
+  });
+  int ge = gt | eq << 16;   // inclusive prefix over the lanes (both below 2^16)
+  uint32_t s = (uint32_t)ge;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int g2 = __shfl_up_sync(0xffffffffu, g, o), e2 = __shfl_up_sync(0xffffffffu, e, o);
-    if (lane >= o) {
-      g += g2;
-      e += e2;
-    }
+    const uint32_t y = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s += y;
   }
-  if (lane == 31) {
-    wsum[warp][0] = g;
-    wsum[warp][1] = e;
+  uint32_t before = 0, gall;
+  if (nw > 1) {
+    __syncthreads();   // the rounds' last counts have been read
+    if (lane == 31) cnt[0][warp][0] = s;
+    __syncthreads();
+    const uint32_t c = lane < nw ? cnt[0][lane][0] : 0u;
+    before = __reduce_add_sync(0xffffffffu, lane < warp ? c : 0u);
+    gall = __reduce_add_sync(0xffffffffu, c) & 0xffffu;
+  } else {
+    gall = __shfl_sync(0xffffffffu, s, 31) & 0xffffu;
   }
-  __syncthreads();
-  int gb = 0, eb = 0, gall = 0;
-  for (int w = 0; w < (nt >> 5); ++w) {
-    if (w < warp) {
-      gb += wsum[w][0];
-      eb += wsum[w][1];
-    }
-    gall += wsum[w][0];
-  }
-  const int want = take - gall;   // how many of the equal ones
-  int gi = gb + g - gt, ei = eb + e - eq;
-  for (int i = i0; i < i1; ++i) {
-    const uint32_t kk = key[i];
+  s += before - (uint32_t)ge;   // exclusive
+  const int want = take - (int)gall;   // how many of the equal ones
+  int gi = s & 0xffffu, ei = s >> 16;
+  each([&](int i, uint32_t kk) {
     if (kk > v) {
       out[gi + min(ei, want)] = i;
       ++gi;
@@ -438,7 +558,7 @@ __global__ void __launch_bounds__(1024) block_select_kernel(const float *scores,
       if (ei < want) out[gi + ei] = i;
       ++ei;
     }
-  }
+  });
 }
 
 }  // namespace
@@ -466,7 +586,7 @@ cudaError_t launch_block_keys(const mla_config &cfg, const void *cache, long lon
 
 ScoreLayout score_layout(const mla_config &cfg, int B, int key_blocks) {
   ScoreLayout L;
-  L.head_rows = (cfg.n_h + 127) / 128 * 128;
+  L.head_rows = (cfg.n_h + 31) / 32 * 32;
   L.tiles = (key_blocks + kScoreTile - 1) / kScoreTile;
   L.logit_off = 0;
   size_t off = align_up(sizeof(float) * (size_t)B * L.tiles * kScoreTile * L.head_rows, 256);
@@ -476,42 +596,49 @@ ScoreLayout score_layout(const mla_config &cfg, int B, int key_blocks) {
   return L;
 }
 
-cudaError_t launch_block_scores(const mla_config &cfg, bool tc, float scale_log2, const void *q_abs, const void *keys,
-                                int key_blocks, const int *ctx_len, int B, float *scores, char *ws,
-                                const ScoreLayout &L, unsigned *status, cudaStream_t s) {
-  if (B > 65535 || cfg.n_h > 8 * 65535 || L.tiles == 0) return cudaErrorNotSupported;
+cudaError_t launch_block_scores_tc(const mla_config &cfg, float scale_log2, const void *q_abs, const void *keys,
+                                   int key_blocks, const int *ctx_len, int B, float *scores, unsigned *status,
+                                   cudaStream_t s) {
+  const int tiles = (key_blocks + kScoreTile - 1) / kScoreTile;
+  if (B > 65535 || cfg.d_c + cfg.d_r != 576 || cfg.dtype != MLA_BF16 || tiles > kSMaxTiles * kSMaxCluster ||
+      ((uintptr_t)q_abs | (uintptr_t)keys) % 16 != 0)
+    return cudaErrorNotSupported;
+  CUtensorMap mq, mk;
+  const uint64_t dq[3] = {576, (uint64_t)cfg.n_h, (uint64_t)B}, dk[3] = {576, (uint64_t)key_blocks, (uint64_t)B};
+  const uint64_t sq[2] = {1152, 1152ull * cfg.n_h}, sk[2] = {1152, 1152ull * key_blocks};
+  const uint32_t box[3] = {64, 128, 1};
+  if (!encode_map_bf16(&mq, q_abs, 3, dq, sq, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_map_bf16(&mk, keys, 3, dk, sk, box, CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorNotSupported;
+  static std::atomic<int> configured[kMaxDevices];
+  const cudaError_t e = once_per_device(configured, [] {
+    return cudaFuncSetAttribute(score_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSSmem);
+  });
+  if (e != cudaSuccess) return e;
+  const int cluster = tiles > 4 ? 8 : (tiles > 2 ? 4 : tiles);
+  const int per = (tiles + cluster - 1) / cluster;
+  const int stages = kSRing / ((1 + per) * 16384);
+  const uint32_t cols = per == 1 ? 128 : (per == 2 ? 256 : 512);
+  return launch_pdl(score_tc_kernel, dim3(cluster, B), dim3(kSThreads), kSSmem, s, cluster, mq, mk, key_blocks, ctx_len,
+                    cfg.n_h, scale_log2, scores, per, stages, cols, status);
+}
+
+cudaError_t launch_block_scores_simt(const mla_config &cfg, float scale_log2, const void *q_abs, const void *keys,
+                                     int key_blocks, const int *ctx_len, int B, float *scores, char *ws,
+                                     const ScoreLayout &L, unsigned *status, cudaStream_t s) {
+  const size_t smem = sizeof(float) * cfg.n_h;
+  if (B > 65535 || smem > 48 * 1024 || L.tiles == 0) return cudaErrorNotSupported;
   float *logits = reinterpret_cast<float *>(ws + L.logit_off);
   float2 *stats = reinterpret_cast<float2 *>(ws + L.stat_off);
   const int D = cfg.d_c + cfg.d_r;
-  cudaError_t e;
-  if (tc) {
-    if (D != 576 || cfg.dtype != MLA_BF16 || ((uintptr_t)q_abs | (uintptr_t)keys) % 16 != 0) return cudaErrorNotSupported;
-    CUtensorMap mq, mk;
-    const uint64_t dq[3] = {576, (uint64_t)cfg.n_h, (uint64_t)B}, dk[3] = {576, (uint64_t)key_blocks, (uint64_t)B};
-    const uint64_t sq[2] = {1152, 1152ull * cfg.n_h}, sk[2] = {1152, 1152ull * key_blocks};
-    const uint32_t box[3] = {64, 128, 1};
-    if (!encode_map_bf16(&mq, q_abs, 3, dq, sq, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !encode_map_bf16(&mk, keys, 3, dk, sk, box, CU_TENSOR_MAP_SWIZZLE_128B))
-      return cudaErrorNotSupported;
-    static std::atomic<int> configured[kMaxDevices];
-    e = once_per_device(configured, [] {
-      return cudaFuncSetAttribute(score_logits_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSSmem);
-    });
-    if (e != cudaSuccess) return e;
-    e = launch_pdl(score_logits_tc_kernel, dim3(L.tiles, L.head_rows / 128, B), dim3(kSThreads), kSSmem, s, 1, mq, mk,
-                   key_blocks, ctx_len, cfg.n_h, scale_log2, logits, stats, L, status);
-  } else {
-    const dim3 grid(L.tiles, (cfg.n_h + 7) / 8, B);
-    e = cfg.dtype == MLA_FP32
-            ? launch_pdl(score_logits_simt_kernel<float>, grid, dim3(256), 0, s, 1, (const float *)q_abs,
-                         (const float *)keys, key_blocks, ctx_len, cfg.n_h, D, scale_log2, logits, stats, L)
-            : launch_pdl(score_logits_simt_kernel<__nv_bfloat16>, grid, dim3(256), 0, s, 1,
-                         (const __nv_bfloat16 *)q_abs, (const __nv_bfloat16 *)keys, key_blocks, ctx_len, cfg.n_h, D,
-                         scale_log2, logits, stats, L);
-  }
+  const dim3 grid(L.tiles, (cfg.n_h + 7) / 8, B);
+  const cudaError_t e =
+      cfg.dtype == MLA_FP32
+          ? launch_pdl(score_logits_simt_kernel<float>, grid, dim3(256), 0, s, 1, (const float *)q_abs,
+                       (const float *)keys, key_blocks, ctx_len, cfg.n_h, D, scale_log2, logits, stats, L)
+          : launch_pdl(score_logits_simt_kernel<__nv_bfloat16>, grid, dim3(256), 0, s, 1, (const __nv_bfloat16 *)q_abs,
+                       (const __nv_bfloat16 *)keys, key_blocks, ctx_len, cfg.n_h, D, scale_log2, logits, stats, L);
   if (e != cudaSuccess) return e;
-  const size_t smem = sizeof(float) * cfg.n_h;
-  if (smem > 48 * 1024) return cudaErrorNotSupported;
   return launch_pdl(score_sum_kernel, dim3((key_blocks + kSumBlocks - 1) / kSumBlocks, B), dim3(256), smem, s, 1,
                     (const float *)logits, (const float2 *)stats, L, key_blocks, ctx_len, cfg.n_h, scores, status);
 }
@@ -519,14 +646,18 @@ cudaError_t launch_block_scores(const mla_config &cfg, bool tc, float scale_log2
 cudaError_t launch_block_select(const float *scores, int n_blocks, const int *ctx_len, int B, int k, int n_first,
                                 int n_last, int *sel, int *n_sel, unsigned *status, cudaStream_t s) {
   if (n_blocks > kSelMaxBlocks) return cudaErrorNotSupported;
+  if (n_blocks <= 1024 * kSelRegs) {
+    const int threads = std::max(32, (n_blocks + 32 * kSelRegs - 1) / (32 * kSelRegs) * 32);
+    return launch_pdl(block_select_kernel<true>, dim3(B), dim3(threads), 0, s, 1, scores, n_blocks, ctx_len, k, n_first,
+                      n_last, sel, n_sel, status);
+  }
   static std::atomic<int> configured[kMaxDevices];
   const cudaError_t e = once_per_device(configured, [] {
-    return cudaFuncSetAttribute(block_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelMaxBlocks * 4);
+    return cudaFuncSetAttribute(block_select_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                kSelMaxBlocks * 4);
   });
   if (e != cudaSuccess) return e;
-  // about four blocks to a thread: fewer warps to meet at each round's barrier
-  const int threads = std::min(1024, std::max(32, (n_blocks + 127) / 128 * 32));
-  return launch_pdl(block_select_kernel, dim3(B), dim3(threads), sizeof(uint32_t) * (size_t)n_blocks, s, 1, scores,
+  return launch_pdl(block_select_kernel<false>, dim3(B), dim3(1024), sizeof(uint32_t) * (size_t)n_blocks, s, 1, scores,
                     n_blocks, ctx_len, k, n_first, n_last, sel, n_sel, status);
 }
 

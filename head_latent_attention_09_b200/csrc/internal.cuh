@@ -361,17 +361,20 @@ cudaError_t launch_tree_accept(const mla_config &cfg, void *cache, long long cac
 cudaError_t launch_block_keys(const mla_config &cfg, const void *cache, long long cache_len, const int *block_table,
                               int max_blocks, const int *ctx_begin, const int *ctx_len, int B, int max_new, void *keys,
                               int key_blocks, unsigned *status, cudaStream_t s);
-struct ScoreLayout {
-  size_t logit_off;   // float [B, head_rows, blocks rounded up to 128]
-  size_t stat_off;    // float2 [B, block tiles, head_rows]: a tile's maximum and sum of exponentials
+struct ScoreLayout {   // workspace of the CUDA-core kernels
+  size_t logit_off;    // float [B, blocks rounded up to 128, head_rows]
+  size_t stat_off;     // float2 [B, block tiles, head_rows]: a tile's maximum and sum of exponentials
   size_t total;
-  int head_rows;      // heads rounded up to 128
-  int tiles;          // 128-block tiles
+  int head_rows;       // heads rounded up to 32
+  int tiles;           // 128-block tiles
 };
 ScoreLayout score_layout(const mla_config &cfg, int B, int key_blocks);
-cudaError_t launch_block_scores(const mla_config &cfg, bool tc, float scale_log2, const void *q_abs, const void *keys,
-                                int key_blocks, const int *ctx_len, int B, float *scores, char *ws,
-                                const ScoreLayout &L, unsigned *status, cudaStream_t s);
+cudaError_t launch_block_scores_tc(const mla_config &cfg, float scale_log2, const void *q_abs, const void *keys,
+                                   int key_blocks, const int *ctx_len, int B, float *scores, unsigned *status,
+                                   cudaStream_t s);
+cudaError_t launch_block_scores_simt(const mla_config &cfg, float scale_log2, const void *q_abs, const void *keys,
+                                     int key_blocks, const int *ctx_len, int B, float *scores, char *ws,
+                                     const ScoreLayout &L, unsigned *status, cudaStream_t s);
 cudaError_t launch_block_select(const float *scores, int n_blocks, const int *ctx_len, int B, int k, int n_first,
                                 int n_last, int *sel, int *n_sel, unsigned *status, cudaStream_t s);
 

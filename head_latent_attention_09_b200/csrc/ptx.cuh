@@ -339,6 +339,11 @@ __device__ __forceinline__ float4 ld_shared_cluster_v4f(uint32_t addr) {
                : "memory");
   return v;
 }
+__device__ __forceinline__ float2 ld_shared_cluster_v2f(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+  return v;
+}
 __device__ __forceinline__ void fence_acq_rel_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
 __device__ __forceinline__ void fence_proxy_async_cluster() {
   asm volatile("fence.proxy.async.shared::cluster;" ::: "memory");

@@ -659,10 +659,14 @@ cudaError_t launch_tree_attn_simt(const AttnArgs &a, int P, bool fp32, cudaStrea
   return cudaGetLastError();
 }
 
-// Vectorised combine for d_c a multiple of 4 and at most 512: one warp per
-// (sequence, head), 8 per block.  The warp reduces the pieces' log-sum-exps
-// across its lanes, then each lane accumulates up to four float4 columns of
-// the weighted partials, with the loads of several pieces in flight at once.
+// Vectorised combine for d_c a multiple of 4 and at most 512: `segs` warps per
+// (sequence, head), each for 128 / segs of every 128 float4 columns, 8 warps
+// per block.  A warp reduces the pieces' log-sum-exps across its lanes; then
+// the lanes compute the weights of 32 pieces at a time, one each, and pass them
+// round by shuffles while the loads of kMergeAhead pieces are in flight.  With
+// many rows one warp each fills the GPU; with few (long contexts split many
+// times) four warps a row and the loads in flight take the place of the missing
+// rows (4 sequences x 16 heads x 37 pieces: 32 -> 8 us).
 template <typename T>
 __device__ __forceinline__ void store4(T *dst, float4 v);
 template <>
@@ -678,13 +682,17 @@ __device__ __forceinline__ void store4<__nv_bfloat16>(__nv_bfloat16 *dst, float4
   *reinterpret_cast<uint2 *>(dst) = u;
 }
 
-template <typename T>
+constexpr int kMergeAhead = 8;
+template <typename T, int kPer>   // float4 columns of a lane: 4 (one warp a row) or 1 (four warps a row)
 __global__ void __launch_bounds__(256) combine_vec_kernel(const char *ws, WsLayout L, int B, int n_h, int d_c,
                                                           T *ctx_lat, float *lse_out) {
   pdl_trigger();
   pdl_wait();
+  constexpr int kSegs = 4 / kPer;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long row = (long long)blockIdx.x * 8 + warp;   // = b * n_h + h
+  const long long unit = (long long)blockIdx.x * 8 + warp;
+  const long long row = unit / kSegs;   // = b * n_h + h
+  const int f0 = (int)(unit % kSegs) * 32 * kPer + lane;
   if (row >= (long long)B * n_h) return;
   const int b = (int)(row / n_h), h = (int)(row % n_h);
   const long long *pb = reinterpret_cast<const long long *>(ws + L.piece_base_off);
@@ -698,39 +706,50 @@ __global__ void __launch_bounds__(256) combine_vec_kernel(const char *ws, WsLayo
   T *dst = ctx_lat + row * d_c;
   const int n4 = d_c / 4;
   if (m == -CUDART_INF_F) {
-    for (int f = lane; f < n4; f += 32) store4<T>(dst + 4 * f, make_float4(0.f, 0.f, 0.f, 0.f));
-    if (lse_out && lane == 0) lse_out[row] = -CUDART_INF_F;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (f0 + 32 * i < n4) store4<T>(dst + 4 * (f0 + 32 * i), make_float4(0.f, 0.f, 0.f, 0.f));
+    if (lse_out && f0 == 0) lse_out[row] = -CUDART_INF_F;
     return;
   }
   float tot = 0.f;
   for (long long p = p0 + lane; p < p1; p += 32) tot += expf(lse[part_row(L, p, h)] - m);
   tot = warp_sum(tot);
   const float inv = 1.f / tot;
-  float4 acc[4];
+  float4 acc[kPer];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (long long p = p0; p < p1; ++p) {
-    const float w = expf(lse[part_row(L, p, h)] - m) * inv;
-    const float4 *src = reinterpret_cast<const float4 *>(op + part_row(L, p, h) * (long long)d_c);
+  for (int i = 0; i < kPer; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  constexpr int kAhead = kPer == 1 ? kMergeAhead : kMergeAhead / 2;
+  for (long long q0 = p0; q0 < p1; q0 += 32) {
+    const int n = (int)min(32ll, p1 - q0);
+    const float wl = lane < n ? expf(lse[part_row(L, q0 + lane, h)] - m) * inv : 0.f;
+    for (int j0 = 0; j0 < n; j0 += kAhead) {
+      float4 v[kAhead][kPer];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int f = lane + 32 * i;
-      if (f < n4) {
-        const float4 v = __ldg(src + f);
-        acc[i].x += w * v.x;
-        acc[i].y += w * v.y;
-        acc[i].z += w * v.z;
-        acc[i].w += w * v.w;
+      for (int j = 0; j < kAhead; ++j) {
+        const float4 *src = reinterpret_cast<const float4 *>(op + part_row(L, q0 + j0 + j, h) * (long long)d_c);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+          v[j][i] = j0 + j < n && f0 + 32 * i < n4 ? __ldg(src + f0 + 32 * i) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        const float w = __shfl_sync(0xffffffffu, wl, (j0 + j) & 31);
+        if (j0 + j >= n) continue;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          acc[i].x += w * v[j][i].x;
+          acc[i].y += w * v[j][i].y;
+          acc[i].z += w * v[j][i].z;
+          acc[i].w += w * v[j][i].w;
+        }
       }
     }
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int f = lane + 32 * i;
-    if (f < n4) store4<T>(dst + 4 * f, acc[i]);
-  }
-  if (lse_out && lane == 0) lse_out[row] = m + logf(tot);
+  for (int i = 0; i < kPer; ++i)
+    if (f0 + 32 * i < n4) store4<T>(dst + 4 * (f0 + 32 * i), acc[i]);
+  if (lse_out && f0 == 0) lse_out[row] = m + logf(tot);
 }
 
 cudaError_t launch_combine(const mla_config &cfg, const char *ws, const WsLayout &L, int B,
@@ -740,13 +759,17 @@ cudaError_t launch_combine(const mla_config &cfg, const char *ws, const WsLayout
   if (cfg.d_c % 4 == 0 && cfg.d_c <= 512 && ((uintptr_t)ctx_lat % (4 * esz)) == 0 &&
       ((uintptr_t)ws % 16) == 0) {
     const long long rows = (long long)B * cfg.n_h;
-    const unsigned blocks = (unsigned)((rows + 7) / 8);
+    // Four warps a row while that is still at most about one resident set of
+    // warps (148 SMs x 64): more rows fill the GPU with one warp each.
+    const bool split = rows <= 2048;
+    const unsigned blocks = (unsigned)((rows * (split ? 4 : 1) + 7) / 8);
+    auto go = [&](auto kern, auto *out) {
+      return launch_pdl(kern, dim3(blocks), dim3(256), 0, s, 1, ws, L, B, cfg.n_h, cfg.d_c, out, lse);
+    };
     if (f32)
-      return launch_pdl(combine_vec_kernel<float>, dim3(blocks), dim3(256), 0, s, 1, ws, L, B, cfg.n_h, cfg.d_c,
-                        (float *)ctx_lat, lse);
-    else
-      return launch_pdl(combine_vec_kernel<__nv_bfloat16>, dim3(blocks), dim3(256), 0, s, 1, ws, L, B, cfg.n_h,
-                        cfg.d_c, (__nv_bfloat16 *)ctx_lat, lse);
+      return split ? go(combine_vec_kernel<float, 1>, (float *)ctx_lat) : go(combine_vec_kernel<float, 4>, (float *)ctx_lat);
+    return split ? go(combine_vec_kernel<__nv_bfloat16, 1>, (__nv_bfloat16 *)ctx_lat)
+                 : go(combine_vec_kernel<__nv_bfloat16, 4>, (__nv_bfloat16 *)ctx_lat);
   }
   dim3 grid(B, cfg.n_h);
   if (f32)

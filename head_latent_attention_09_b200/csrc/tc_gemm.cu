@@ -581,12 +581,15 @@ cudaError_t launch_gemm(const CUtensorMap &a0, const CUtensorMap &a1, const CUte
 }
 
 // K split: the smallest power of two (<= 8, the portable cluster size) that
-// gives at least one CTA per SM, while every slice keeps >= 2 K chunks.
-int pick_ksplit(long long ctas, int num_k_chunks) {
+// gives at least one CTA per SM, while every slice keeps >= 2 K chunks.  Tiles
+// of 256 columns take an SM's shared memory each, so there the split stops
+// before a second wave (1024 tokens of d = 5120: 20 CTAs x 8 in two waves 28
+// us, x 4 in one 20 us).
+int pick_ksplit(long long ctas, int num_k_chunks, int bn) {
   int sms = 148, dev = 0;
   if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   int ks = 1;
-  while (ks < 8 && ctas * ks < sms && num_k_chunks >= 4 * ks) ks *= 2;
+  while (ks < 8 && ctas * ks < sms && num_k_chunks >= 4 * ks && (bn < 256 || 2 * ctas * ks <= sms)) ks *= 2;
   return ks;
 }
 
@@ -612,7 +615,7 @@ cudaError_t dispatch(int N, GemmParams g, int mtiles, int z, cudaStream_t s, Enc
   const int ntiles = (N + bn - 1) / bn;
   if (g.mt_per_cta == 0) g.mt_per_cta = 1;
   if (g.ksplit == 0)
-    g.ksplit = g.mt_per_cta > 1 ? 1 : pick_ksplit((long long)mtiles * ntiles * z, g.num_k_chunks);
+    g.ksplit = g.mt_per_cta > 1 ? 1 : pick_ksplit((long long)mtiles * ntiles * z, g.num_k_chunks, bn);
   const int per = (g.num_k_chunks + g.ksplit - 1) / g.ksplit;
   g.group = pick_group(per, bn, g.mt_per_cta);
   Maps m;

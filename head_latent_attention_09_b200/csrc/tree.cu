@@ -14,9 +14,11 @@ template <> __device__ __forceinline__ __nv_bfloat16 cast<__nv_bfloat16>(float x
 // Log-sum-exp merge of the groups that are split between shares.  A share
 // boundary cuts at most one plan sequence (gang groups), so block x takes
 // member x % gang of the one that begins in share x / gang and runs on into
-// the next (if there is one); y counts blocks of 8 query rows, one warp each.
+// the next (if there is one); y counts blocks of 8 warps, one warp for 128
+// columns of a query row, with the loads of kMergeAhead partials in flight.
 // Groups that lie in one share were written by the attention kernel, so the
 // traffic is that of at most 2 P gang pieces however many groups there are.
+constexpr int kMergeAhead = 4;
 template <typename T>
 __global__ void __launch_bounds__(256) tree_combine_kernel(AttnArgs a) {
   pdl_trigger();
@@ -44,7 +46,8 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(AttnArgs a) {
   const int v = reinterpret_cast<const int *>(a.ws + a.L.share_first_off)[w0 + 1];
   const long long s0 = tp[v], s1 = tp[v + 1];
   if (s0 >= plan_begin(w0 + 1, P, Ttot) || s0 < plan_begin(w0, P, Ttot)) return;   // begins elsewhere
-  const int r = blockIdx.y * 8 + warp;
+  const int unit = blockIdx.y * 8 + warp, segs = (a.d_c + 127) / 128;
+  const int r = unit / segs, f0 = unit % segs * 128 + lane;   // query row of the group; columns f0, f0 + 32, ..
   const int b = v / a.tree.runs, g = (v - b * a.tree.runs) * a.tree.gang + member;
   const int row = g * a.tree.group_rows + r;   // past the sequence's rows where there is no group g
   if (r >= a.tree.group_rows || row >= a.tree.seq_rows) return;
@@ -64,24 +67,31 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(AttnArgs a) {
   for (int o = 16; o > 0; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
   const float inv = tot == 0.f ? 0.f : 1.f / tot;
   const long long orow = (long long)b * a.tree.seq_rows + row;
-  for (int f0 = 0; f0 < a.d_c; f0 += 512) {
-    float acc[16];
+  float acc[4] = {0.f, 0.f, 0.f, 0.f};
+  for (long long q0 = w0; q0 <= w1; q0 += 32) {
+    const int n = (int)min(32ll, w1 + 1 - q0);
+    const float wl = lane < n ? expf(lse[part(q0 + lane)] - m_use) * inv : 0.f;
+    for (int j0 = 0; j0 < n; j0 += kMergeAhead) {
+      float v[kMergeAhead][4];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) acc[i] = 0.f;
-#pragma unroll 2
-    for (long long w = w0; w <= w1; ++w) {
-      const long long pr = part(w);
-      const float wt = expf(lse[pr] - m_use) * inv;
-      const float *src = op + pr * a.d_c + f0;
+      for (int j = 0; j < kMergeAhead; ++j) {
+        const float *src = op + (j0 + j < n ? part(q0 + j0 + j) * a.d_c : 0);
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (f0 + lane + 32 * i < a.d_c) acc[i] += wt * src[lane + 32 * i];
+        for (int i = 0; i < 4; ++i) v[j][i] = j0 + j < n && f0 + 32 * i < a.d_c ? src[f0 + 32 * i] : 0.f;
+      }
+#pragma unroll
+      for (int j = 0; j < kMergeAhead; ++j) {
+        const float wt = __shfl_sync(0xffffffffu, wl, (j0 + j) & 31);
+        if (j0 + j >= n) continue;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i] += wt * v[j][i];
+      }
     }
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (f0 + lane + 32 * i < a.d_c) out[orow * a.d_c + f0 + lane + 32 * i] = cast<T>(acc[i]);
   }
-  if (a.tree.lse && lane == 0) a.tree.lse[orow] = tot == 0.f ? -CUDART_INF_F : m_use + logf(tot);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (f0 + 32 * i < a.d_c) out[orow * a.d_c + f0 + 32 * i] = cast<T>(acc[i]);
+  if (a.tree.lse && f0 == 0) a.tree.lse[orow] = tot == 0.f ? -CUDART_INF_F : m_use + logf(tot);
 }
 
 // Accepted path: row cached + path[i] -> cached + i, one block per sequence.
@@ -142,7 +152,7 @@ cudaError_t accept_units(int row_bytes, void *cache, const AttnArgs &a, const in
 }  // namespace
 
 cudaError_t launch_tree_combine(const AttnArgs &a, int P, bool fp32, cudaStream_t s) {
-  const dim3 grid(P * a.tree.gang, (a.tree.group_rows + 7) / 8);
+  const dim3 grid(P * a.tree.gang, (a.tree.group_rows * ((a.d_c + 127) / 128) + 7) / 8);
   if (grid.y > 65535) return cudaErrorNotSupported;
   return fp32 ? launch_pdl(tree_combine_kernel<float>, grid, dim3(256), 0, s, 1, a)
               : launch_pdl(tree_combine_kernel<__nv_bfloat16>, grid, dim3(256), 0, s, 1, a);

@@ -86,7 +86,7 @@ def scores_of(sh, h, q, keys, ctx, blocks):
     return host(out)
 
 
-@pytest.mark.parametrize("blocks", [1, 5, 127, 128, 129, 300, 2049])
+@pytest.mark.parametrize("blocks", [1, 5, 127, 128, 129, 300, 520, 1100, 2049, 3900])
 @pytest.mark.parametrize("sh", [shape(LITE), shape(V2), shape(V2, n_h=200), shape(TINY), shape(ODD)])
 def test_block_scores(sh, blocks):
     rng = np.random.default_rng(blocks)
@@ -102,6 +102,28 @@ def test_block_scores(sh, blocks):
     got = scores_of(sh, h, q, given, ctx, blocks)
     ok(h)
     M.mla_destroy(h)
+    compare_scores(sh, got, q, keys, ctx)
+
+
+def test_block_scores_beyond_the_tensor_core_kernel():
+    """More than 4096 blocks run on the CUDA cores (strict mode refuses)."""
+    sh = shape(LITE)
+    rng = np.random.default_rng(0)
+    ctx = [64 * 4100 - 5, 70]
+    keys = stored(sh, rng.standard_normal((2, 4100, 576)))
+    q = stored(sh, rng.standard_normal((2, 16, 576)) * 0.7)
+    h = handle(sh, strict=True)
+    with pytest.raises(M.MlaError) as e:
+        scores_of(sh, h, q, keys, ctx, 4100)
+    assert e.value.status == M.MLA_ERR_UNSUPPORTED
+    M.mla_set_strict(h, 0)
+    got = scores_of(sh, h, q, keys, ctx, 4100)
+    ok(h)
+    M.mla_destroy(h)
+    compare_scores(sh, got, q, keys, ctx)
+
+
+def compare_scores(sh, got, q, keys, ctx):
     scale = O.softmax_scale(sh["d_h"], sh["d_r"])
     for b, n in enumerate(ctx):
         nb = -(-n // 64)
