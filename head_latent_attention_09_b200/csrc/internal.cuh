@@ -318,12 +318,12 @@ __device__ __forceinline__ long long token_row(const AttnArgs &a, int b, long lo
   return (long long)blk * a.page_size + ((unsigned)t - bi * (unsigned)a.page_size);
 }
 
-// The same for token t of a sequence's selected blocks.  -1 also for a block
-// that the sequence does not have, and for its partial last block anywhere
-// but at the end of the selection (end: the selected tokens).
-__device__ __forceinline__ long long selected_row(const AttnArgs &a, int b, long long t, int end) {
+// The same for token t of a sequence's selected blocks, of `cached` tokens in
+// all.  -1 also for a block that the sequence does not have, and for its
+// partial last block anywhere but at the end of the selection (end: the
+// selected tokens).
+__device__ __forceinline__ long long selected_row(const AttnArgs &a, int b, long long t, int end, int cached) {
   const int blk = a.sel[(long long)b * a.sel_k + t / kTile];
-  const int cached = plan_cached(a, b);
   if (blk < 0 || (long long)blk * kTile >= cached) return -1;
   if (((long long)blk + 1) * kTile > cached && t / kTile != (end - 1) / kTile) return -1;
   return token_row(a, b, (long long)blk * kTile + t % kTile);

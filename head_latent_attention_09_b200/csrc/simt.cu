@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(256) attn_simt_kernel(AttnArgs a) {
     const long long p_begin = beg + (s0 - tp[b]) * a.plan_tile;
     const long long p_end = min((long long)ctx, beg + (s1 - tp[b]) * a.plan_tile);
     const int seq = kTree ? b / a.tree.T : b;
-    const int cached = kTree ? plan_cached(a, b) : 0;
+    const int cached = kTree || a.sel ? plan_cached(a, b) : 0;
     const unsigned long long bits = kTree ? a.tree.mask[b] : 0ull;
 
     float q[kQPerLane];
@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(256) attn_simt_kernel(AttnArgs a) {
 
     for (long long p = p_begin; p < p_end; ++p) {
       if (kTree && p >= cached && !((bits >> (p - cached)) & 1ull)) continue;
-      const long long row = a.sel ? selected_row(a, b, p, ctx) : token_row(a, seq, p);
+      const long long row = a.sel ? selected_row(a, b, p, ctx, cached) : token_row(a, seq, p);
       if (row < 0) {
         if (lane == 0) atomicOr(a.status, kStatusBounds);
         continue;

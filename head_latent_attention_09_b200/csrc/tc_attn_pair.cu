@@ -111,7 +111,7 @@ struct Piece {
   int tok_begin;       // first token of the piece in sequence b
   int tok_end;         // one past the last token attended by this piece
   int ctx;             // the sequence's context length (clamped to the cache)
-  int cached;          // tokens before the drafted ones (ctx without a tree)
+  int cached;          // tokens before a tree's drafted ones; of the sequence, where blocks of it are selected
   int ntiles;          // 256-token MMA tiles
 };
 
@@ -155,7 +155,7 @@ __device__ __forceinline__ bool walk_next(Walk &w, const AttnArgs &a, int share,
     if (kTree && pc.g >= a.tree.groups) continue;
     const int ctx = plan_ctx(a.ws, a.L, b);
     const int beg = kTree ? 0 : plan_begin_tok(a, b);
-    pc.cached = kTree ? plan_cached(a, b) : ctx;
+    pc.cached = kTree || a.sel ? plan_cached(a, b) : ctx;
     pc.piece = w.pb[b] + (share - plan_share_of_tile(w.tp[b], w.P, w.Ttot));
     pc.tok_begin = beg + (int)((s0 - w.tp[b]) * a.plan_tile);
     const long long e = beg + (s1 - w.tp[b]) * a.plan_tile;
@@ -165,12 +165,6 @@ __device__ __forceinline__ bool walk_next(Walk &w, const AttnArgs &a, int share,
     return true;
   }
   return false;
-}
-
-// Cache row of token t of the piece's sequence, or -1 (unmapped / outside the cache).
-template <bool kTree>
-__device__ __forceinline__ long long kv_row(const AttnArgs &a, const Piece &p, int t) {
-  return !kTree && a.sel ? selected_row(a, p.b, t, p.ctx) : token_row(a, p.b, t);
 }
 
 // The k lowest bits (none for k <= 0, all from 32 on).
@@ -215,18 +209,48 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, unsign
   return ok;
 }
 
-// Row coordinate of a block of cache rows starting at token t0 of the piece's
-// sequence, or an out-of-range row (TMA then fills zeros) when the block
-// starts past the piece.
+// Row coordinates of the four 64-token blocks of the tile at token t0 of a
+// piece: an out-of-range row (TMA then fills zeros) for a block past the piece
+// and, marked in `bad`, for one that is unmapped, outside the cache or not a
+// block of the sequence (see selected_row).  The table and selection entries
+// of all four are requested before any is used, and nothing branches on them.
+struct Rows {
+  int r[4];
+  unsigned bad;
+};
 template <bool kTree>
-__device__ __forceinline__ int block_row(const AttnArgs &a, const Piece &p, int t0, long long kv_rows) {
-  if (t0 >= p.tok_end) return (int)kv_rows;
-  const long long r = kv_row<kTree>(a, p, t0);
-  if (r < 0) {
-    atomicOr(a.status, kStatusBounds);
-    return (int)kv_rows;
+__device__ __forceinline__ Rows look_up(const AttnArgs &a, const Piece &p, int t0, int kv_rows) {
+  Rows x;
+  x.bad = 0;
+  const bool chosen = !kTree && a.sel != nullptr;
+  int blk[4];
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    blk[t] = t0 / kTile + t;
+    if (chosen && t0 + kTile * t < p.tok_end) blk[t] = a.sel[(long long)p.b * a.sel_k + blk[t]];
   }
-  return (int)r;
+  bool ok[4];
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    ok[t] = true;
+    if (chosen) {
+      const long long e = (long long)blk[t] * kTile;
+      ok[t] = blk[t] >= 0 && e < p.cached && (e + kTile <= p.cached || t0 / kTile + t == (p.ctx - 1) / kTile);
+    }
+    if (a.page_size) {
+      ok[t] = ok[t] && blk[t] < a.max_blocks;
+      if (ok[t] && t0 + kTile * t < p.tok_end) blk[t] = a.block_table[(long long)p.b * a.max_blocks + blk[t]];
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    if (a.page_size) ok[t] = ok[t] && blk[t] >= 0 && blk[t] < a.cache_len;
+    const bool here = t0 + kTile * t < p.tok_end;
+    const long long row = (a.page_size ? 0 : (long long)p.b * a.cache_len) + (long long)blk[t] * kTile;
+    x.r[t] = here && ok[t] ? (int)row : kv_rows;
+    x.bad |= here && !ok[t] ? 1u << t : 0u;
+  }
+  return x;
 }
 
 // O += P V sub-stages of a tile that starts at token t0 of the piece (the
@@ -329,15 +353,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           phase ^= 1u;
         }
       };
-      // The rows of a tile's four 64-token blocks: in the cache, and for P.V
-      // of a tree's last blocks in their copy.
-      struct Rows { int r[4]; };
-      auto look_up = [&](const Piece &p, int t0) {
-        Rows x;
-#pragma unroll
-        for (int t = 0; t < 4; ++t) x.r[t] = block_row<kTree>(a, p, t0 + kSubTok * t, kv_rows);
-        return x;
-      };
       // V sub-stages of the tile at token t0 of piece p: tokens t0 + 64t..,
       // latent columns 256g + 128 * rank .. +128, one 3D box: 64 rows x both
       // 64-column chunks.
@@ -385,11 +400,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           else
             ptx::tma_load_2d_pair(sQ + c * 8192, &mapQ, lq, 64 * c, pc.b * 128 + 64 * (int)rank);
         }
-        Rows next = look_up(pc, pc.tok_begin);
+        Rows next = look_up<kTree>(a, pc, pc.tok_begin, (int)kv_rows);
         for (int k = 0; k < pc.ntiles && ok; ++k) {
           const int t0 = pc.tok_begin + kTileTok * k;
           x = next;
-          if (k + 1 < pc.ntiles) next = look_up(pc, t0 + kTileTok);
+          if (x.bad) atomicOr(a.status, kStatusBounds);
           // K chunks of this tile: this CTA's 128 tokens x 64 columns each.
           const int y0 = rank ? x.r[2] : x.r[0], y1 = rank ? x.r[3] : x.r[1];
 #pragma unroll 1
@@ -406,6 +421,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             step();
           }
           if (!ok) break;
+          if (k + 1 < pc.ntiles) next = look_up<kTree>(a, pc, t0 + kTileTok, (int)kv_rows);
           if (vpending && !issue_v(vpc, vt0, vx)) { ok = false; break; }
           vpc = pc;
           vt0 = t0;

@@ -131,6 +131,7 @@ struct Piece {
   int b;
   long long piece;
   int tok_begin, tok_end, ctx, ntiles;
+  int cached;   // selected blocks: the sequence's cached tokens
 };
 
 struct Walk {
@@ -169,6 +170,7 @@ __device__ __forceinline__ bool walk_next(Walk &w, const AttnArgs &a, int share,
     const long long e = beg + (s1 - w.tp[b]) * a.plan_tile;
     pc.tok_end = (int)(e < ctx ? e : ctx);
     pc.ctx = ctx;
+    pc.cached = a.sel ? plan_cached(a, b) : ctx;
     pc.ntiles = (pc.tok_end - pc.tok_begin + kTileTok - 1) / kTileTok;
     return true;
   }
@@ -176,7 +178,7 @@ __device__ __forceinline__ bool walk_next(Walk &w, const AttnArgs &a, int share,
 }
 
 __device__ __forceinline__ long long kv_row(const AttnArgs &a, const Piece &p, int t) {
-  return a.sel ? selected_row(a, p.b, t, p.ctx) : token_row(a, p.b, t);
+  return a.sel ? selected_row(a, p.b, t, p.ctx, p.cached) : token_row(a, p.b, t);
 }
 
 // Row coordinate of the 64-row block of cache rows starting at token t0 of the
@@ -353,13 +355,13 @@ __global__ void __launch_bounds__(Cfg<H, F8>::kThreads, 1)
         // its rows), wholly past its end (TMA from an out-of-range row: zeros),
         // or holding its end (hand copy).
         int kind[2], yy[2];
+        int y = (int)kv_rows;   // lane h2: the row of half h2, both lookups at once
+        if (lane < 2 && tok0 + 64 * lane + 64 <= pc.ctx) y = block_row(a, pc, tok0 + 64 * lane, kv_rows);
 #pragma unroll
         for (int h2 = 0; h2 < 2; ++h2) {
           const int t = tok0 + 64 * h2;
           kind[h2] = t + 64 <= pc.ctx ? 0 : (t >= pc.ctx ? 1 : 2);
-          int y = (int)kv_rows;
-          if (kind[h2] == 0 && lane == 0) y = block_row(a, pc, t, kv_rows);
-          yy[h2] = __shfl_sync(0xffffffffu, y, 0);
+          yy[h2] = __shfl_sync(0xffffffffu, y, h2);
         }
         const bool whole = a.page_size == 0 && !a.sel && kind[0] == 0 && kind[1] == 0 && yy[0] < kv_rows &&
                            yy[1] == yy[0] + 64;
