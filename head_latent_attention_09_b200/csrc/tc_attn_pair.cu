@@ -586,16 +586,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int nvalid = min(max(pc.tok_end - base, 0), 64);
         if (!warp_wait(bars.sfull(i & 1), (i >> 1) & 1, a.status, abort_flag)) { ok = false; break; }
         ptx::tc_fence_after();
-        // This thread's 64 scores, in log2 units, invalid tokens at -inf.
+        // This thread's 64 products, invalid tokens at -inf.  The scale to log2
+        // units is positive, so the maximum is taken first and the scale
+        // joins the subtraction in one (two-wide) multiply-add: the kernel
+        // runs into the board's power limit, and every instruction a score
+        // costs counts.
         float v[64];
         ptx::tmem_ld64_sync(lane_addr + (i & 1) * kColS + 64 * hf, reinterpret_cast<uint32_t *>(v));
         float mx[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
         if (base + 64 <= (kTree ? min(pc.cached, pc.tok_end) : pc.tok_end)) {
 #pragma unroll
-          for (int j = 0; j < 64; ++j) {
-            v[j] *= a.scale_log2;
-            mx[j & 3] = fmaxf(mx[j & 3], v[j]);
-          }
+          for (int j = 0; j < 64; ++j) mx[j & 3] = fmaxf(mx[j & 3], v[j]);
         } else {
           uint32_t valid[2];
 #pragma unroll
@@ -603,7 +604,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             valid[w2] = kTree ? tree_valid(w2, base, nvalid, pc.cached, bits) : low_bits(nvalid - 32 * w2);
 #pragma unroll
           for (int j = 0; j < 64; ++j) {
-            v[j] = (valid[j >> 5] >> (j & 31)) & 1u ? v[j] * a.scale_log2 : -CUDART_INF_F;
+            v[j] = (valid[j >> 5] >> (j & 31)) & 1u ? v[j] : -CUDART_INF_F;
             mx[j & 3] = fmaxf(mx[j & 3], v[j]);
           }
         }
@@ -613,7 +614,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(bars.xchg(i & 1));
         if (!warp_wait(bars.xchg(i & 1), (i >> 1) & 1, a.status, abort_flag)) { ok = false; break; }
-        const float m_tile = fmaxf(fmaxf(rm[h], rm[64 + h]), fmaxf(rm[128 + h], rm[192 + h]));
+        const float m_tile = fmaxf(fmaxf(rm[h], rm[64 + h]), fmaxf(rm[128 + h], rm[192 + h])) * a.scale_log2;
         bool rescale = false;
         float alpha = 1.f;
         if (m_tile > m_run + kRescale) {
@@ -629,15 +630,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // A row with nothing valid so far (a tree's masks) subtracts 0: -inf - -inf is NaN.
         const float m_use = kTree && m_run == -CUDART_INF_F ? 0.f : m_run;
         uint32_t pk[32];
-        float ps[4] = {0.f, 0.f, 0.f, 0.f};
+        float2 ps[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
+        const float2 scale2 = {a.scale_log2, a.scale_log2}, m2 = {-m_use, -m_use};
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
-          const float p0 = ptx::exp2_approx(v[2 * j] - m_use), p1 = ptx::exp2_approx(v[2 * j + 1] - m_use);
-          ps[j & 3] += p0 + p1;
-          __nv_bfloat162 b2 = __floats2bfloat162_rn(p0, p1);
+          float2 p = ptx::fma2({v[2 * j], v[2 * j + 1]}, scale2, m2);
+          p.x = ptx::exp2_approx(p.x);
+          p.y = ptx::exp2_approx(p.y);
+          ps[j & 3] = ptx::add2(ps[j & 3], p);
+          __nv_bfloat162 b2 = __float22bfloat162_rn(p);
           pk[j] = *reinterpret_cast<uint32_t *>(&b2);
         }
-        l_part += (ps[0] + ps[1]) + (ps[2] + ps[3]);
+        const float2 sum2 = ptx::add2(ptx::add2(ps[0], ps[1]), ptx::add2(ps[2], ps[3]));
+        l_part += sum2.x + sum2.y;
         // P of the previous tile must have been read by its P.V.
         if (i >= 1 && !warp_wait(bars.pfree(), (i - 1) & 1, a.status, abort_flag)) { ok = false; break; }
         // Tokens 8u .. of the chunk are 16-byte unit u of row h (128-byte swizzle by row).
