@@ -136,18 +136,26 @@ def _ptr(x):
     raise TypeError(f"cannot pass {type(x).__name__} as a pointer")
 
 
-_current_stream = None      # torch.cuda.current_stream, once a GPU has been seen
+_raw_stream = None      # returns the current stream's handle; set once a GPU has been seen
+
+
+def _find_raw_stream():
+    import torch
+    if not torch.cuda.is_available():
+        return None
+    raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+    if raw is None or device is None:
+        return lambda: torch.cuda.current_stream().cuda_stream
+    torch.cuda.init()
+    return lambda: raw(device())      # the same handle without a Stream object (0.2 instead of 3 us a call)
 
 
 def _stream(s):
     if s is None:
-        global _current_stream
-        if _current_stream is None:
-            import torch
-            if not torch.cuda.is_available():
-                return None
-            _current_stream = torch.cuda.current_stream
-        return _current_stream().cuda_stream
+        global _raw_stream
+        if _raw_stream is None:
+            _raw_stream = _find_raw_stream()
+        return _raw_stream() if _raw_stream is not None else None
     if isinstance(s, int):
         return s
     return s.cuda_stream

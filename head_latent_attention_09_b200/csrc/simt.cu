@@ -76,6 +76,7 @@ __device__ long long block_exclusive_scan(long long v, long long *smem, long lon
 __device__ void make_plan(const PlanSource &src, int B, int P_req, long long cap, int tile, char *ws,
                           const WsLayout &L, unsigned *status) {
   __shared__ long long scan[32];
+  __shared__ long long prefix[1025];   // the tile prefix of up to 1024 plan sequences, for the search below
   long long *tile_prefix = reinterpret_cast<long long *>(ws + L.tile_prefix_off);
   long long *piece_base = reinterpret_cast<long long *>(ws + L.piece_base_off);
   int *ctx_eff = reinterpret_cast<int *>(ws + L.ctx_off);   // [B] ends, then [B] first tokens
@@ -137,14 +138,19 @@ __device__ void make_plan(const PlanSource &src, int B, int P_req, long long cap
   long long run = block_exclusive_scan(local, scan, &Ttot);
   for (int b = b0; b < b1; ++b) {
     tile_prefix[b] = run;
+    if (B <= 1024) prefix[b] = run;
     run += tiles_of(b);
   }
-  if (tid == 0) tile_prefix[B] = Ttot;
+  if (tid == 0) {
+    tile_prefix[B] = Ttot;
+    if (B <= 1024) prefix[B] = Ttot;
+  }
+  const long long *tpre = B <= 1024 ? prefix : tile_prefix;
   const long long P = Ttot < (long long)P_req ? Ttot : (long long)P_req;
 
   long long local_pieces = 0;
   for (int b = b0; b < b1; ++b) {
-    long long s = tile_prefix[b];
+    long long s = tpre[b];
     long long t = tiles_of(b);
     if (t > 0) local_pieces += plan_share_of_tile(s + t - 1, P, Ttot) - plan_share_of_tile(s, P, Ttot) + 1;
   }
@@ -152,7 +158,7 @@ __device__ void make_plan(const PlanSource &src, int B, int P_req, long long cap
   long long prun = block_exclusive_scan(local_pieces, scan, &n_pieces);
   for (int b = b0; b < b1; ++b) {
     piece_base[b] = prun;
-    long long s = tile_prefix[b];
+    long long s = tpre[b];
     long long t = tiles_of(b);
     if (t > 0) prun += plan_share_of_tile(s + t - 1, P, Ttot) - plan_share_of_tile(s, P, Ttot) + 1;
   }
@@ -165,7 +171,7 @@ __device__ void make_plan(const PlanSource &src, int B, int P_req, long long cap
     int lo = 0, hi = B;
     while (lo < hi) {
       const int mid = (lo + hi) >> 1;
-      if (tile_prefix[mid + 1] <= t0) lo = mid + 1; else hi = mid;
+      if (tpre[mid + 1] <= t0) lo = mid + 1; else hi = mid;
     }
     share_first[w] = lo;
   }
