@@ -135,12 +135,18 @@ namespace mla {
 // share is empty, which makes the pieces of one sequence a run of consecutive
 // shares.
 // ---------------------------------------------------------------------------
+// a / b of non-negative values, in 32 bits where both fit (a 64-bit division
+// costs some hundred cycles, and every role of every kernel walks the plan).
+__host__ __device__ inline long long plan_div(long long a, long long b) {
+  if (((unsigned long long)(a | b) >> 32) == 0) return (unsigned)a / (unsigned)b;
+  return a / b;
+}
 __host__ __device__ inline long long plan_begin(long long w, long long P, long long Ttot) {
-  return w * Ttot / P;
+  return plan_div(w * Ttot, P);
 }
 // Largest share index whose range starts at or before tile t (0 <= t < Ttot).
 __host__ __device__ inline long long plan_share_of_tile(long long t, long long P, long long Ttot) {
-  return ((t + 1) * P - 1) / Ttot;
+  return plan_div((t + 1) * P - 1, Ttot);
 }
 __host__ __device__ inline long long ceil_div_ll(long long a, long long b) { return (a + b - 1) / b; }
 

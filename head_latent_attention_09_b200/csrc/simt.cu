@@ -76,7 +76,9 @@ __device__ long long block_exclusive_scan(long long v, long long *smem, long lon
 __device__ void make_plan(const PlanSource &src, int B, int P_req, long long cap, int tile, char *ws,
                           const WsLayout &L, unsigned *status) {
   __shared__ long long scan[32];
-  __shared__ long long prefix[1025];   // the tile prefix of up to 1024 plan sequences, for the search below
+  // the tile counts and their prefix for up to 1024 plan sequences (a thread each)
+  __shared__ long long prefix[1025];
+  __shared__ int ntiles[1024];
   long long *tile_prefix = reinterpret_cast<long long *>(ws + L.tile_prefix_off);
   long long *piece_base = reinterpret_cast<long long *>(ws + L.piece_base_off);
   int *ctx_eff = reinterpret_cast<int *>(ws + L.ctx_off);   // [B] ends, then [B] first tokens
@@ -119,7 +121,9 @@ __device__ void make_plan(const PlanSource &src, int B, int P_req, long long cap
       }
       ctx_eff[b] = (int)end;
       beg_eff[b] = (int)c;
-      local += ceil_div_ll(end, tile);
+      const long long t = ceil_div_ll(end, tile);
+      if (B <= 1024) ntiles[b] = (int)t;
+      local += t;
       continue;
     }
     long long g = src.ctx_begin ? src.ctx_begin[b] : 0;
@@ -130,10 +134,14 @@ __device__ void make_plan(const PlanSource &src, int B, int P_req, long long cap
     }
     ctx_eff[b] = (int)c;
     beg_eff[b] = (int)g;
-    local += ceil_div_ll(c - g, tile);
+    const long long t = ceil_div_ll(c - g, tile);
+    if (B <= 1024) ntiles[b] = (int)t;
+    local += t;
   }
   const bool from0 = src.drafted > 0 || src.sel;
-  auto tiles_of = [&](int b) { return ceil_div_ll(ctx_eff[b] - (from0 ? 0 : beg_eff[b]), tile); };
+  auto tiles_of = [&](int b) -> long long {
+    return B <= 1024 ? ntiles[b] : ceil_div_ll(ctx_eff[b] - (from0 ? 0 : beg_eff[b]), tile);
+  };
   long long Ttot;
   long long run = block_exclusive_scan(local, scan, &Ttot);
   for (int b = b0; b < b1; ++b) {

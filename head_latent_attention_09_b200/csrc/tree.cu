@@ -14,17 +14,22 @@ template <> __device__ __forceinline__ __nv_bfloat16 cast<__nv_bfloat16>(float x
 // Log-sum-exp merge of the groups that are split between shares.  A share
 // boundary cuts at most one plan sequence (gang groups), so block x takes
 // member x % gang of the one that begins in share x / gang and runs on into
-// the next (if there is one); y counts blocks of 8 warps, one warp for 128
-// columns of a query row, with the loads of kMergeAhead partials in flight.
+// the next (if there is one); y counts blocks of 8 query rows, a warp each.
 // Groups that lie in one share were written by the attention kernel, so the
 // traffic is that of at most 2 P gang pieces however many groups there are.
-constexpr int kMergeAhead = 4;
+// The first two partials of a row (mostly all there are) are requested before
+// their log-sum-exps are used; one wave of blocks covers every share.
 template <typename T>
 __global__ void __launch_bounds__(256) tree_combine_kernel(AttnArgs a) {
   pdl_trigger();
   pdl_wait();
+  const long long w0 = blockIdx.x / a.tree.gang;
+  const int member = blockIdx.x % a.tree.gang;
   const WsHeader *hd = reinterpret_cast<const WsHeader *>(a.ws);
+  const int *share_first = reinterpret_cast<const int *>(a.ws + a.L.share_first_off);
   const long long P = hd->P, Ttot = hd->Ttot;
+  // the plan sequence that holds the first tile of the next share
+  const int v = w0 + 1 < gridDim.x / a.tree.gang ? share_first[w0 + 1] : 0;
   const long long *tp = reinterpret_cast<const long long *>(a.ws + a.L.tile_prefix_off);
   const float *lse = reinterpret_cast<const float *>(a.ws + a.L.lse_off);
   const float *op = reinterpret_cast<const float *>(a.ws + a.L.opart_off);
@@ -39,21 +44,24 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(AttnArgs a) {
     }
     return;
   }
-  const long long w0 = blockIdx.x / a.tree.gang;
-  const int member = blockIdx.x % a.tree.gang;
   if (w0 + 1 >= P) return;
-  // the group that holds the first tile of the next share
-  const int v = reinterpret_cast<const int *>(a.ws + a.L.share_first_off)[w0 + 1];
   const long long s0 = tp[v], s1 = tp[v + 1];
   if (s0 >= plan_begin(w0 + 1, P, Ttot) || s0 < plan_begin(w0, P, Ttot)) return;   // begins elsewhere
-  const int unit = blockIdx.y * 8 + warp, segs = (a.d_c + 127) / 128;
-  const int r = unit / segs, f0 = unit % segs * 128 + lane;   // query row of the group; columns f0, f0 + 32, ..
+  const int r = blockIdx.y * 8 + warp;
   const int b = v / a.tree.runs, g = (v - b * a.tree.runs) * a.tree.gang + member;
   const int row = g * a.tree.group_rows + r;   // past the sequence's rows where there is no group g
   if (r >= a.tree.group_rows || row >= a.tree.seq_rows) return;
   const long long w1 = plan_share_of_tile(s1 - 1, P, Ttot);
   // partials: the last piece of share w0 (or its only one), the first of the others
   auto part = [&](long long w) { return part_row(a.L, tree_piece(a, tp, v, w, member, P, Ttot).slot, r); };
+  const long long pr0 = part(w0), pr1 = part(w0 + 1);
+  float v0[16], v1[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const int f = lane + 32 * i;
+    v0[i] = f < a.d_c ? op[pr0 * a.d_c + f] : 0.f;
+    v1[i] = f < a.d_c ? op[pr1 * a.d_c + f] : 0.f;
+  }
   float m = -CUDART_INF_F;
   for (long long w = w0 + lane; w <= w1; w += 32) m = fmaxf(m, lse[part(w)]);
 #pragma unroll
@@ -66,32 +74,21 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(AttnArgs a) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
   const float inv = tot == 0.f ? 0.f : 1.f / tot;
+  const float wt0 = expf(lse[pr0] - m_use) * inv, wt1 = expf(lse[pr1] - m_use) * inv;
   const long long orow = (long long)b * a.tree.seq_rows + row;
-  float acc[4] = {0.f, 0.f, 0.f, 0.f};
-  for (long long q0 = w0; q0 <= w1; q0 += 32) {
-    const int n = (int)min(32ll, w1 + 1 - q0);
-    const float wl = lane < n ? expf(lse[part(q0 + lane)] - m_use) * inv : 0.f;
-    for (int j0 = 0; j0 < n; j0 += kMergeAhead) {
-      float v[kMergeAhead][4];
 #pragma unroll
-      for (int j = 0; j < kMergeAhead; ++j) {
-        const float *src = op + (j0 + j < n ? part(q0 + j0 + j) * a.d_c : 0);
+  for (int i = 0; i < 16; ++i) v0[i] = wt0 * v0[i] + wt1 * v1[i];
+  for (long long w = w0 + 2; w <= w1; ++w) {
+    const long long pr = part(w);
+    const float wt = expf(lse[pr] - m_use) * inv;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[j][i] = j0 + j < n && f0 + 32 * i < a.d_c ? src[f0 + 32 * i] : 0.f;
-      }
-#pragma unroll
-      for (int j = 0; j < kMergeAhead; ++j) {
-        const float wt = __shfl_sync(0xffffffffu, wl, (j0 + j) & 31);
-        if (j0 + j >= n) continue;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[i] += wt * v[j][i];
-      }
-    }
+    for (int i = 0; i < 16; ++i)
+      if (lane + 32 * i < a.d_c) v0[i] += wt * op[pr * a.d_c + lane + 32 * i];
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (f0 + 32 * i < a.d_c) out[orow * a.d_c + f0 + 32 * i] = cast<T>(acc[i]);
-  if (a.tree.lse && f0 == 0) a.tree.lse[orow] = tot == 0.f ? -CUDART_INF_F : m_use + logf(tot);
+  for (int i = 0; i < 16; ++i)
+    if (lane + 32 * i < a.d_c) out[orow * a.d_c + lane + 32 * i] = cast<T>(v0[i]);
+  if (a.tree.lse && lane == 0) a.tree.lse[orow] = tot == 0.f ? -CUDART_INF_F : m_use + logf(tot);
 }
 
 // Accepted path: row cached + path[i] -> cached + i, one block per sequence.
@@ -152,8 +149,8 @@ cudaError_t accept_units(int row_bytes, void *cache, const AttnArgs &a, const in
 }  // namespace
 
 cudaError_t launch_tree_combine(const AttnArgs &a, int P, bool fp32, cudaStream_t s) {
-  const dim3 grid(P * a.tree.gang, (a.tree.group_rows * ((a.d_c + 127) / 128) + 7) / 8);
-  if (grid.y > 65535) return cudaErrorNotSupported;
+  const dim3 grid(P * a.tree.gang, (a.tree.group_rows + 7) / 8);
+  if (grid.y > 65535 || a.d_c > 512) return cudaErrorNotSupported;
   return fp32 ? launch_pdl(tree_combine_kernel<float>, grid, dim3(256), 0, s, 1, a)
               : launch_pdl(tree_combine_kernel<__nv_bfloat16>, grid, dim3(256), 0, s, 1, a);
 }
