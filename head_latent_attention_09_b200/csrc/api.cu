@@ -295,9 +295,7 @@ int decode_attn(mla_handle *h, const void *q_abs, const void *cache, const float
   if (!workspace || ((uintptr_t)workspace & 255u) || ws_bytes < L.total) return MLA_ERR_WORKSPACE;
   cudaStream_t s = (cudaStream_t)stream;
   const int tile = plan_tile_of(h, kv_scale != nullptr);
-  cudaError_t e = launch_plan(src, B, P, token_cap(c, cache_len, max_blocks_per_seq), tile, (char *)workspace, L,
-                              h->d_status, s);
-  if (e != cudaSuccess) return MLA_ERR_CUDA;
+  const long long cap = token_cap(c, cache_len, max_blocks_per_seq);
   AttnArgs a;
   a.q_abs = q_abs;
   a.cache = cache;
@@ -318,14 +316,24 @@ int decode_attn(mla_handle *h, const void *q_abs, const void *cache, const float
   a.status = h->d_status;
   a.sel = src.sel;
   a.sel_k = src.sel_k;
-  e = cudaErrorNotSupported;
+  a.src = src;
+  a.cap = cap;
+  // The tensor-core kernels plan for themselves, up to kInlineSeqs sequences
+  // (the one for 32 heads over an FP8 cache has no shared memory left for it).
+  const Before plan = [&] { return launch_plan(src, B, P, cap, tile, (char *)workspace, L, h->d_status, s); };
+  a.inline_plan = B <= kInlineSeqs && !(kv_scale && c.n_h > 16);
+  const Before before = a.inline_plan ? Before() : plan;
+  cudaError_t e = cudaErrorNotSupported;
   if (h->attn_kind == kAttnTcPair && !kv_scale && aligned16(q_abs) && aligned16(cache))
-    e = launch_attn_tc_pair(a, P, s);
+    e = launch_attn_tc_pair(a, P, s, before);
   else if (h->attn_kind == kAttnTcSmallH && aligned16(q_abs) && aligned16(cache))
-    e = launch_attn_tc_smallh(a, P, s);
+    e = launch_attn_tc_smallh(a, P, s, before);
   const bool tc_exists = (h->attn_kind == kAttnTcPair && !kv_scale) || h->attn_kind == kAttnTcSmallH;
   if (strict_refuses(h, tc_exists, e)) return MLA_ERR_UNSUPPORTED;
-  if (e == cudaErrorNotSupported) e = launch_attn_simt(a, P, c.dtype == MLA_FP32, s);
+  if (e == cudaErrorNotSupported) {
+    e = plan();
+    if (e == cudaSuccess) e = launch_attn_simt(a, P, c.dtype == MLA_FP32, s);
+  }
   if (e == cudaErrorNotSupported) return MLA_ERR_UNSUPPORTED;
   return from_cuda(e);
 }
@@ -489,7 +497,15 @@ int mla_tree_attn(mla_handle *h, const void *q_abs, const void *cache, long long
     if (tc) {
       // the tensor maps are made before anything is launched
       if (!aligned16(q_abs) || !aligned16(cache) || !aligned16(ctx_lat)) return cudaErrorNotSupported;
-      e = launch_tree_attn_tc_pair(a, t.parts, s, [&] { return launch_tree_plan_copy(src, a, t.parts, cap, s); });
+      a.src = src;
+      a.cap = cap;
+      a.inline_plan = a.B <= kInlineSeqs;
+      e = launch_tree_attn_tc_pair(a, t.parts, s, [&] {
+        // the copy comes last: an in-line plan starts beside it
+        cudaError_t b = cudaSuccess;
+        if (!a.inline_plan) b = launch_plan(src, a.B, t.parts, cap, t.tile, a.ws, a.L, a.status, s);
+        return b == cudaSuccess ? launch_tree_copy(src, a, cap, s) : b;
+      });
     } else {
       e = launch_plan(src, a.B, t.parts, cap, t.tile, a.ws, a.L, a.status, s);
       if (e == cudaSuccess) e = launch_tree_attn_simt(a, t.parts, c.dtype == MLA_FP32, s);

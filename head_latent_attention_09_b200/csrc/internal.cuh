@@ -185,6 +185,9 @@ struct WsLayout {
 
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
+// Plan sequences up to which the tensor-core attention kernels plan in line.
+constexpr int kInlineSeqs = 256;
+
 // Row of (piece, head) in the partials (units of d_c floats) and index of its
 // log-sum-exp.
 __host__ __device__ inline long long part_row(const WsLayout &L, long long piece, int head) {
@@ -276,6 +279,11 @@ struct AttnArgs {
   const int *sel = nullptr;
   int sel_k = 0;
   TreeArgs tree;     // B is then the number of plan sequences (runs x batch)
+  // Tensor-core kernels, B <= kInlineSeqs: every CTA makes the plan itself in
+  // shared memory (plan.cuh) from these instead of reading a plan kernel's.
+  int inline_plan = 0;
+  PlanSource src{nullptr};
+  long long cap = 0;
 };
 
 // ---------------------------------------------------------------------------
@@ -295,23 +303,17 @@ struct AttnArgs {
 cudaError_t launch_plan(const PlanSource &src, int B, int P, long long cap, int tile, char *ws, const WsLayout &L,
                         unsigned *status, cudaStream_t s);
 
-// The plan of a tree for the tensor-core kernel, and in the same launch the
-// copy of the blocks that hold drafted tokens (a: every field but the plan's).
-cudaError_t launch_tree_plan_copy(const PlanSource &src, const AttnArgs &a, int P, long long cap, cudaStream_t s);
+// Tree: the copy of the blocks that hold drafted tokens, for the tensor-core
+// kernel, which starts beside it.
+cudaError_t launch_tree_copy(const PlanSource &src, const AttnArgs &a, long long cap, cudaStream_t s);
 
-// The clamped end (context length) of sequence b, as the plan stored it.
-__device__ __forceinline__ int plan_ctx(const char *ws, const WsLayout &L, int b) {
-  return reinterpret_cast<const int *>(ws + L.ctx_off)[b];
+// The plan stores two values per plan sequence: the end of its attended tokens
+// (clamped), and its first token (a multiple of kTile), or for selected blocks
+// and trees, which start at token 0, the number of its cached tokens.
+__device__ __forceinline__ const int *plan_ends(const AttnArgs &a) {
+  return reinterpret_cast<const int *>(a.ws + a.L.ctx_off);
 }
-// The first attended token of sequence b (a multiple of kTile).
-__device__ __forceinline__ int plan_begin_tok(const AttnArgs &a, int b) {
-  if (a.sel || a.tree.T) return 0;
-  return reinterpret_cast<const int *>(a.ws + a.L.ctx_off)[a.B + b];
-}
-// The cached tokens of plan sequence b (selected blocks and trees).
-__device__ __forceinline__ int plan_cached(const AttnArgs &a, int b) {
-  return reinterpret_cast<const int *>(a.ws + a.L.ctx_off)[a.B + b];
-}
+__device__ __forceinline__ const int *plan_seconds(const AttnArgs &a) { return plan_ends(a) + a.B; }
 
 // Cache row of token t of batch sequence b (t below what the cache can
 // address), or -1 when its page is unmapped or outside the pool.
@@ -441,13 +443,13 @@ cudaError_t launch_linear_tc(const void *x, const void *w, void *y, int M, int K
 cudaError_t launch_combine_outproj_tc(const mla_config &cfg, const char *ws, const WsLayout &L, int B,
                                       const void *w_uv, void *o, void *ctx_lat, float *lse, unsigned *status,
                                       cudaStream_t s);
-cudaError_t launch_attn_tc_pair(const AttnArgs &a, int P, cudaStream_t s);
+// `before` launches what goes before the kernel (a plan, a copy), once the
+// arguments are known to be ones it can take.
+using Before = std::function<cudaError_t()>;
+cudaError_t launch_attn_tc_pair(const AttnArgs &a, int P, cudaStream_t s, const Before &before);
 // The same kernel over a tree of drafted tokens, 128 query rows at a time.
-// `plan` launches what goes before it, once the arguments are known to be ones
-// it can take.
-cudaError_t launch_tree_attn_tc_pair(const AttnArgs &a, int P, cudaStream_t s,
-                                     const std::function<cudaError_t()> &plan);
-cudaError_t launch_attn_tc_smallh(const AttnArgs &a, int P, cudaStream_t s);
+cudaError_t launch_tree_attn_tc_pair(const AttnArgs &a, int P, cudaStream_t s, const Before &before);
+cudaError_t launch_attn_tc_smallh(const AttnArgs &a, int P, cudaStream_t s, const Before &before);
 
 // One bounded wait on a barrier that nothing completes, giving up after
 // limit_ns: sets the status word's time-out bit (self-test of that path).

@@ -5,7 +5,7 @@
 #include <cuda_fp8.h>
 #include <math_constants.h>
 
-#include "internal.cuh"
+#include "plan.cuh"
 
 namespace mla {
 namespace {
@@ -89,56 +89,15 @@ __device__ void make_plan(const PlanSource &src, int B, int P_req, long long cap
 
   long long local = 0;
   for (int b = b0; b < b1; ++b) {
-    // A length outside [0, cap] is flagged and clamped; the tiles below and
-    // every attention kernel use the clamped length.
-    const int seq = src.runs > 1 ? b / src.runs : b;
-    long long c = src.ctx_len[seq];
-    if (c < 0 || c > cap) {
-      atomicOr(status, kStatusBounds);
-      c = c < 0 ? 0 : cap;
-    }
-    if (src.drafted > 0 || src.sel) {
-      // the second value kept is the number of cached tokens; the first token is 0
-      long long end;
-      if (src.sel) {
-        long long n = src.n_sel[seq];
-        const long long most = min((long long)src.sel_k, ceil_div_ll(c, kTile));
-        if (n < 0 || n > most) {
-          atomicOr(status, kStatusBounds);
-          n = n < 0 ? 0 : most;
-        }
-        end = n * kTile;
-        if (n > 0) {
-          const long long last = src.sel[(long long)seq * src.sel_k + n - 1];
-          if (last >= 0 && last * kTile < c) end -= max(0ll, (last + 1) * kTile - c);   // the partial block
-        }
-      } else {
-        end = c + src.drafted;
-        if (end > cap) {
-          atomicOr(status, kStatusBounds);
-          end = cap;
-        }
-      }
-      ctx_eff[b] = (int)end;
-      beg_eff[b] = (int)c;
-      const long long t = ceil_div_ll(end, tile);
-      if (B <= 1024) ntiles[b] = (int)t;
-      local += t;
-      continue;
-    }
-    long long g = src.ctx_begin ? src.ctx_begin[b] : 0;
-    if (g < 0 || g > c || g % kTile != 0) {
-      atomicOr(status, kStatusBounds);
-      g = g < 0 ? 0 : (g > c ? c : g);
-      g -= g % kTile;
-    }
-    ctx_eff[b] = (int)c;
-    beg_eff[b] = (int)g;
-    const long long t = ceil_div_ll(c - g, tile);
+    int end, second;
+    plan_entry(src, b, cap, status, &end, &second);
+    ctx_eff[b] = end;
+    beg_eff[b] = second;
+    const long long t = ceil_div_ll(end - (plan_from0(src) ? 0 : second), tile);
     if (B <= 1024) ntiles[b] = (int)t;
     local += t;
   }
-  const bool from0 = src.drafted > 0 || src.sel;
+  const bool from0 = plan_from0(src);
   auto tiles_of = [&](int b) -> long long {
     return B <= 1024 ? ntiles[b] : ceil_div_ll(ctx_eff[b] - (from0 ? 0 : beg_eff[b]), tile);
   };
@@ -175,13 +134,7 @@ __device__ void make_plan(const PlanSource &src, int B, int P_req, long long cap
   // complete here (the scan above synchronised the block).
   int *share_first = reinterpret_cast<int *>(ws + L.share_first_off);
   for (long long w = tid; w < P; w += nt) {
-    const long long t0 = plan_begin(w, P, Ttot);
-    int lo = 0, hi = B;
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (tpre[mid + 1] <= t0) lo = mid + 1; else hi = mid;
-    }
-    share_first[w] = lo;
+    share_first[w] = plan_first(tpre, B, w, P, Ttot);
   }
   if (tid == 0) {
     piece_base[B] = n_pieces;
@@ -211,18 +164,16 @@ __device__ __forceinline__ uint4 finite_or_zero(uint4 v) {
   return make_uint4(one(v.x), one(v.y), one(v.z), one(v.w));
 }
 
-// Tree: block 0 makes the plan while the others copy the blocks that hold
-// drafted tokens, kCopyBlocks blocks of kCopyRows rows per sequence (rows of
-// 72 16-byte units).
+// Tree: the copy of the blocks that hold drafted tokens, kCopyBlocks blocks of
+// kCopyRows rows per sequence (rows of 72 16-byte units).  The attention kernel
+// starts while this one runs, and waits for it only before it reads a copied
+// block; it may start as soon as the kernels before this one are done, hence
+// the trigger behind the wait.
 constexpr int kCopyRows = 8, kCopyBlocks = kTreeCopyRows / kCopyRows;
-__global__ void __launch_bounds__(1024) tree_plan_copy_kernel(PlanSource src, AttnArgs a, int P_req, long long cap) {
-  pdl_trigger();
+__global__ void __launch_bounds__(288) tree_copy_kernel(PlanSource src, AttnArgs a, long long cap) {
   pdl_wait();
-  if (blockIdx.x == 0) {
-    make_plan(src, a.B, P_req, cap, a.plan_tile, a.ws, a.L, a.status);
-    return;
-  }
-  const int b = (blockIdx.x - 1) / kCopyBlocks, r0 = (blockIdx.x - 1) % kCopyBlocks * kCopyRows;
+  pdl_trigger();
+  const int b = blockIdx.x / kCopyBlocks, r0 = blockIdx.x % kCopyBlocks * kCopyRows;
   const long long cached = min(max((long long)src.ctx_len[b], 0ll), cap);
   const long long end = min(cached + src.drafted, cap);
   const long long first = cached / kTile * kTile;
@@ -288,12 +239,12 @@ __global__ void __launch_bounds__(256) attn_simt_kernel(AttnArgs a) {
     const long long s1 = t1 < tp[b + 1] ? t1 : tp[b + 1];
     if (s0 >= s1) continue;
     const long long piece = pb[b] + (w - plan_share_of_tile(tp[b], P, Ttot));
-    const int ctx = plan_ctx(a.ws, a.L, b);
-    const long long beg = plan_begin_tok(a, b);
+    const int ctx = plan_ends(a)[b];
+    const long long beg = kTree || a.sel ? 0 : plan_seconds(a)[b];
     const long long p_begin = beg + (s0 - tp[b]) * a.plan_tile;
     const long long p_end = min((long long)ctx, beg + (s1 - tp[b]) * a.plan_tile);
     const int seq = kTree ? b / a.tree.T : b;
-    const int cached = kTree || a.sel ? plan_cached(a, b) : 0;
+    const int cached = kTree || a.sel ? plan_seconds(a)[b] : 0;
     const unsigned long long bits = kTree ? a.tree.mask[b] : 0ull;
 
     float q[kQPerLane];
@@ -645,11 +596,10 @@ cudaError_t launch_plan(const PlanSource &src, int B, int P, long long cap, int 
   return launch_pdl(plan_kernel, dim3(1), dim3(threads), 0, s, 1, src, B, P, cap, tile, ws, L, status);
 }
 
-cudaError_t launch_tree_plan_copy(const PlanSource &src, const AttnArgs &a, int P, long long cap, cudaStream_t s) {
-  const int batch = a.B / src.runs;
-  if (a.d_c + a.d_r != 576 || src.drafted > kTreeMaxDrafted) return cudaErrorNotSupported;
-  const int threads = a.B >= 1024 ? 1024 : (a.B <= 288 ? 288 : (a.B + 31) / 32 * 32);
-  return launch_pdl(tree_plan_copy_kernel, dim3(1 + batch * kCopyBlocks), dim3(threads), 0, s, 1, src, a, P, cap);
+cudaError_t launch_tree_copy(const PlanSource &src, const AttnArgs &a, long long cap, cudaStream_t s) {
+  const long long blocks = (long long)(a.B / src.runs) * kCopyBlocks;
+  if (a.d_c + a.d_r != 576 || src.drafted > kTreeMaxDrafted || blocks > 0x7fffffffLL) return cudaErrorNotSupported;
+  return launch_pdl(tree_copy_kernel, dim3((unsigned)blocks), dim3(288), 0, s, 1, src, a, cap);
 }
 
 cudaError_t launch_attn_simt(const AttnArgs &a, int P, bool fp32, cudaStream_t s) {

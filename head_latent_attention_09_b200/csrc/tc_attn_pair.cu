@@ -53,6 +53,7 @@
 // kernel winds down without further waits.
 #include <math_constants.h>
 
+#include "plan.cuh"
 #include "ptx.cuh"
 
 namespace mla {
@@ -87,10 +88,12 @@ constexpr int kBarODone = kBarPFree + 1;        // [2] both: pair commit after P
 constexpr int kBarOFree = kBarODone + 2;        // leader: 16 warp arrivals
 constexpr int kBarXchg = kBarOFree + 1;         // [2] local: 8 softmax-warp arrivals (row-max exchange)
 constexpr int kBarLsum = kBarXchg + 2;          // local: 8 softmax-warp arrivals (row-sum exchange)
-constexpr int kBarEnd = kBarLsum + 1;           // [2] local: the loads of a sequence's last partial block
-constexpr int kNumBars = kBarEnd + 2;
+constexpr int kBarEnd = kBarLsum + 1;           // [2][2] local: the two loads of a sequence's last partial block
+constexpr int kNumBars = kBarEnd + 4;
 constexpr int kOffMisc = kOffBar + kNumBars * 8;
-constexpr int kSmemBytes = kOffMisc + 32;
+constexpr int kOffPlan = kOffMisc + 32;
+constexpr int kSmemBytes = kOffPlan + (int)sizeof(PlanSmem);
+static_assert(kOffPlan % 8 == 0, "the plan holds 64-bit values");
 constexpr int kSmemAlloc = kSmemBytes + 1024;
 static_assert(kSmemAlloc <= 232448, "shared memory budget");
 static_assert(kOffRing % 1024 == 0 && kOffP % 1024 == 0 && kSlot % 1024 == 0,
@@ -118,27 +121,26 @@ struct Piece {
 struct Walk {
   const long long *tp;
   const long long *pb;
+  const int *ends, *seconds;
   long long P, Ttot, t0, t1;
   int b;
   int B;
   int member;   // tree: which of the share's workers this is
 };
 
-__device__ __forceinline__ void walk_init(Walk &w, const AttnArgs &a, int share) {
-  const WsHeader *hd = reinterpret_cast<const WsHeader *>(a.ws);
-  w.P = hd->P;
-  w.Ttot = hd->Ttot;
-  w.tp = reinterpret_cast<const long long *>(a.ws + a.L.tile_prefix_off);
-  w.pb = reinterpret_cast<const long long *>(a.ws + a.L.piece_base_off);
+__device__ __forceinline__ void walk_init(Walk &w, const AttnArgs &a, const PlanView &v, int share) {
+  w.P = v.P;
+  w.Ttot = v.Ttot;
+  w.tp = v.tp;
+  w.pb = v.pb;
+  w.ends = v.ends;
+  w.seconds = v.seconds;
   w.B = a.B;
   w.member = (blockIdx.x >> 1) % a.tree.gang;
-  if (share >= w.P) {
-    w.b = a.B;
-    return;
-  }
+  w.b = v.first;
+  if (share >= w.P) return;
   w.t0 = plan_begin(share, w.P, w.Ttot);
   w.t1 = plan_begin(share + 1, w.P, w.Ttot);
-  w.b = reinterpret_cast<const int *>(a.ws + a.L.share_first_off)[share];   // found by the plan
 }
 
 // Next piece of this share; false when done.
@@ -153,9 +155,9 @@ __device__ __forceinline__ bool walk_next(Walk &w, const AttnArgs &a, int share,
     pc.v = b;
     pc.g = kTree ? (b - pc.b * a.tree.runs) * a.tree.gang + w.member : 0;
     if (kTree && pc.g >= a.tree.groups) continue;
-    const int ctx = plan_ctx(a.ws, a.L, b);
-    const int beg = kTree ? 0 : plan_begin_tok(a, b);
-    pc.cached = kTree || a.sel ? plan_cached(a, b) : ctx;
+    const int ctx = w.ends[b];
+    const int beg = kTree || a.sel ? 0 : w.seconds[b];
+    pc.cached = kTree || a.sel ? w.seconds[b] : ctx;
     pc.piece = w.pb[b] + (share - plan_share_of_tile(w.tp[b], w.P, w.Ttot));
     pc.tok_begin = beg + (int)((s0 - w.tp[b]) * a.plan_tile);
     const long long e = beg + (s1 - w.tp[b]) * a.plan_tile;
@@ -194,7 +196,7 @@ struct Bars {
   __device__ uint64_t *ofree() { return b + kBarOFree; }
   __device__ uint64_t *xchg(int i) { return b + kBarXchg + i; }
   __device__ uint64_t *lsum() { return b + kBarLsum; }
-  __device__ uint64_t *end(int g) { return b + kBarEnd + g; }
+  __device__ uint64_t *end(int n, int g) { return b + kBarEnd + 2 * (n & 1) + g; }
 };
 
 // Warp-uniform bounded wait: lane 0 waits, the result is broadcast, the other
@@ -275,7 +277,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   Bars bars{reinterpret_cast<uint64_t *>(sm + kOffBar)};
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + kOffMisc);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + kOffMisc + 4);
-  int *end_slot = reinterpret_cast<int *>(sm + kOffMisc + 8);   // [2] ring slots of a last partial block
+  int *end_slot = reinterpret_cast<int *>(sm + kOffMisc + 8);   // [2][2] ring slots of a last partial block
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = ptx::cluster_ctarank();
@@ -295,7 +297,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       ptx::mbar_init(bars.odone(i), 1);
       ptx::mbar_init(bars.xchg(i), kSoftmaxWarps);
     }
-    for (int i = 0; i < 2; ++i) ptx::mbar_init(bars.end(i), 1);
+    for (int i = 0; i < 4; ++i) ptx::mbar_init(bars.end(i >> 1, i & 1), 1);
     ptx::mbar_init(bars.pfull(), 2 * kSoftmaxWarps);
     ptx::mbar_init(bars.pfree(), 1);
     ptx::mbar_init(bars.ofree(), 2 * kSoftmaxWarps);
@@ -311,9 +313,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   ptx::cluster_sync_all();
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  // The set-up above overlaps the previous kernel; from here on the plan,
-  // the query and the cache it wrote are read.
-  pdl_wait();
+  // The set-up above overlaps the previous kernel; from here on the lengths,
+  // the query and the cache it wrote are read.  A tree that plans in line runs
+  // behind the copy of its last blocks, which starts it once the kernels before
+  // that copy are done: only the copied blocks are waited for, by the producer.
+  const bool late_wait = kTree && a.inline_plan;
+  if (!late_wait) pdl_wait();
+  PlanSmem &plan_smem = *reinterpret_cast<PlanSmem *>(sm + kOffPlan);
+  const PlanView view = plan_view(a, share, kTree ? gridDim.x / (2 * a.tree.gang) : gridDim.x / 2, plan_smem);
 
   if (warp == 0) {
     // --------------------------------------------------------------- producer
@@ -336,7 +343,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       ptx::tma_prefetch_desc(&mapV2);
       if (kTree) ptx::tma_prefetch_desc(&mapT);
       Walk w;
-      walk_init(w, a, share);
+      walk_init(w, a, view, share);
       const uint64_t last_read = ptx::l2_policy_evict_first();
       int slot = 0;              // ring slot of the next job
       uint32_t phase = 1;        // parity of its empty barrier to wait for (the first round passes at once)
@@ -356,8 +363,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // V sub-stages of the tile at token t0 of piece p: tokens t0 + 64t..,
       // latent columns 256g + 128 * rank .. +128, one 3D box: 64 rows x both
       // 64-column chunks.
+      bool waited = !late_wait;
+      int nend = 0;              // partial blocks so far
       auto issue_v = [&](const Piece &p, int t0, const Rows &x) -> bool {
         const int nsub = tile_subs(p, t0);
+        if (kTree && !waited && t0 + kTileTok > p.cached) {
+          pdl_wait();   // the copy is complete
+          waited = true;
+        }
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
           if (t >= nsub) break;
@@ -372,11 +385,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (!kTree && tok0 + kSubTok > p.ctx) {
               // The block runs past the sequence: its load completes on a
               // barrier of its own, where the helper warp waits, which zeroes
-              // the rows past the end and then arrives for this CTA.
+              // the rows past the end and then arrives for this CTA.  Such
+              // blocks follow one another at once only where a share's last
+              // two tiles both have one (no K chunks come between their V), so
+              // with two sets of barriers and slot numbers the set's previous
+              // block lies more than a ring back and has been consumed.
               if (!ptx::mbar_wait(bars.empty(slot), phase, a.status, abort_flag)) return false;
-              end_slot[g] = slot;
-              ptx::mbar_arrive_expect_tx(bars.end(g), kSlot);
-              ptx::tma_load_3d(dst, map, bars.end(g), 0, y, chunk0);
+              end_slot[2 * (nend & 1) + g] = slot;
+              ptx::mbar_arrive_expect_tx(bars.end(nend, g), kSlot);
+              ptx::tma_load_3d(dst, map, bars.end(nend, g), 0, y, chunk0);
+              if (g == 1) ++nend;
             } else {
               if (!take()) return false;
               ptx::tma_load_3d_pair_hint(dst, map, lf0 + 8 * slot, 0, y, chunk0, last_read);
@@ -439,7 +457,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (!kTree) {
       const uint32_t lf0 = ptx::leader_addr(bars.full(0));
       Walk w;
-      walk_init(w, a, share);
+      walk_init(w, a, view, share);
       Piece pc;
       int n = 0;
       bool ok = true;
@@ -447,8 +465,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int row0 = pc.ctx % kSubTok;
         if (pc.tok_end != pc.ctx || row0 == 0) continue;
         for (int g = 0; g < 2; ++g) {
-          if (!warp_wait(bars.end(g), n & 1, a.status, abort_flag)) { ok = false; break; }
-          const int s = end_slot[g];
+          if (!warp_wait(bars.end(n, g), (n >> 1) & 1, a.status, abort_flag)) { ok = false; break; }
+          const int s = end_slot[2 * (n & 1) + g];
           uint8_t *dst = sRing + s * kSlot;
           for (int u = lane; u < (kSubTok - row0) * 16; u += 32)
             *reinterpret_cast<uint4 *>(dst + (u & 8) * 1024 + (row0 + (u >> 4)) * 128 + (u & 7) * 16) =
@@ -465,7 +483,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const bool issuer = ptx::elect_one();
     if (leader && issuer) {
       Walk w;
-      walk_init(w, a, share);
+      walk_init(w, a, view, share);
       Piece pc;
       int npc = 0, i = 0;
       int rs = 0;                 // ring slot of the next job
@@ -568,7 +586,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     float *lse_out = reinterpret_cast<float *>(a.ws + a.L.lse_off);
     uint8_t *prow = sP + part * 8192 + h * 128;   // this row of the thread's 64-token P chunk
     Walk w;
-    walk_init(w, a, share);
+    walk_init(w, a, view, share);
     Piece pc;
     int i = 0, npc_s = 0;
     bool ok = true;
@@ -769,6 +787,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
 
   // ---------------------------------------------------------------- teardown
+  if (late_wait) pdl_wait();   // what follows this kernel may rely on the copy's being done too
   ptx::tc_fence_before();
   __syncwarp();
   ptx::cluster_sync_all();
@@ -782,7 +801,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
 namespace {
 template <bool kTree>
-cudaError_t launch_pair(const AttnArgs &a, int P, cudaStream_t s, const std::function<cudaError_t()> *before) {
+cudaError_t launch_pair(const AttnArgs &a, int P, cudaStream_t s, const Before &before) {
   if (a.d_c != 512 || a.d_r != 64) return cudaErrorNotSupported;
   if (a.page_size != 0 && a.page_size != kTile) return cudaErrorNotSupported;
   const int batch = kTree ? a.B / a.tree.runs : a.B;
@@ -815,21 +834,20 @@ cudaError_t launch_pair(const AttnArgs &a, int P, cudaStream_t s, const std::fun
   cudaError_t e = once_per_device(configured, [] {
     return cudaFuncSetAttribute(attn_pair_kernel<kTree>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemAlloc);
   });
-  if (e == cudaSuccess && before) e = (*before)();
+  if (e == cudaSuccess && before) e = before();
   if (e != cudaSuccess) return e;
   return launch_pdl(attn_pair_kernel<kTree>, dim3(2 * P * a.tree.gang), dim3(kThreads), kSmemAlloc, s, 1, mq, mk, mv, mv2, mt, a,
                     rows);
 }
 }  // namespace
 
-cudaError_t launch_attn_tc_pair(const AttnArgs &a, int P, cudaStream_t s) {
+cudaError_t launch_attn_tc_pair(const AttnArgs &a, int P, cudaStream_t s, const Before &before) {
   if (a.n_h != 128) return cudaErrorNotSupported;
-  return launch_pair<false>(a, P, s, nullptr);
+  return launch_pair<false>(a, P, s, before);
 }
 
-cudaError_t launch_tree_attn_tc_pair(const AttnArgs &a, int P, cudaStream_t s,
-                                     const std::function<cudaError_t()> &plan) {
-  return launch_pair<true>(a, P, s, &plan);
+cudaError_t launch_tree_attn_tc_pair(const AttnArgs &a, int P, cudaStream_t s, const Before &before) {
+  return launch_pair<true>(a, P, s, before);
 }
 
 }  // namespace mla

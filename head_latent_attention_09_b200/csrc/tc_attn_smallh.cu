@@ -47,6 +47,7 @@
 #include <cuda_fp8.h>
 #include <math_constants.h>
 
+#include "plan.cuh"
 #include "ptx.cuh"
 
 namespace mla {
@@ -108,7 +109,9 @@ struct Cfg {
                        bODone = bPFree + 2, bOFree = bODone + 2, bXchg = bOFree + 1, bLsum = bXchg + 2,
                        kNumBars = bLsum + 1;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
-  static constexpr int kSmem = kOffMisc + 16 + 1024;
+  static constexpr int kOffPlan = (kOffMisc + 16 + 7) / 8 * 8;
+  // (32 heads over an FP8 cache leave no room for an in-line plan.)
+  static constexpr int kSmem = kOffPlan + (F8 && H > 16 ? 0 : (int)sizeof(PlanSmem)) + 1024;
   static constexpr uint32_t kTmemCols = 6 * H <= 128 ? 128 : 256;   // S^T 2 x H, O^T 4 x H
   static constexpr uint32_t kColO = 2 * H;
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
@@ -136,24 +139,23 @@ struct Piece {
 
 struct Walk {
   const long long *tp, *pb;
+  const int *ends, *seconds;
   long long P, Ttot, t0, t1;
   int b, B;
 };
 
-__device__ __forceinline__ void walk_init(Walk &w, const AttnArgs &a, int share) {
-  const WsHeader *hd = reinterpret_cast<const WsHeader *>(a.ws);
-  w.P = hd->P;
-  w.Ttot = hd->Ttot;
-  w.tp = reinterpret_cast<const long long *>(a.ws + a.L.tile_prefix_off);
-  w.pb = reinterpret_cast<const long long *>(a.ws + a.L.piece_base_off);
+__device__ __forceinline__ void walk_init(Walk &w, const AttnArgs &a, const PlanView &v, int share) {
+  w.P = v.P;
+  w.Ttot = v.Ttot;
+  w.tp = v.tp;
+  w.pb = v.pb;
+  w.ends = v.ends;
+  w.seconds = v.seconds;
   w.B = a.B;
-  if (share >= w.P) {
-    w.b = a.B;
-    return;
-  }
+  w.b = v.first;
+  if (share >= w.P) return;
   w.t0 = plan_begin(share, w.P, w.Ttot);
   w.t1 = plan_begin(share + 1, w.P, w.Ttot);
-  w.b = reinterpret_cast<const int *>(a.ws + a.L.share_first_off)[share];   // found by the plan
 }
 
 __device__ __forceinline__ bool walk_next(Walk &w, const AttnArgs &a, int share, Piece &pc) {
@@ -162,15 +164,15 @@ __device__ __forceinline__ bool walk_next(Walk &w, const AttnArgs &a, int share,
     const long long s0 = w.t0 > w.tp[b] ? w.t0 : w.tp[b];
     const long long s1 = w.t1 < w.tp[b + 1] ? w.t1 : w.tp[b + 1];
     if (s0 >= s1) continue;
-    const int ctx = plan_ctx(a.ws, a.L, b);
-    const int beg = plan_begin_tok(a, b);
+    const int ctx = w.ends[b];
+    const int beg = a.sel ? 0 : w.seconds[b];
     pc.b = b;
     pc.piece = w.pb[b] + (share - plan_share_of_tile(w.tp[b], w.P, w.Ttot));
     pc.tok_begin = beg + (int)((s0 - w.tp[b]) * a.plan_tile);
     const long long e = beg + (s1 - w.tp[b]) * a.plan_tile;
     pc.tok_end = (int)(e < ctx ? e : ctx);
     pc.ctx = ctx;
-    pc.cached = a.sel ? plan_cached(a, b) : ctx;
+    pc.cached = a.sel ? w.seconds[b] : ctx;
     pc.ntiles = (pc.tok_end - pc.tok_begin + kTileTok - 1) / kTileTok;
     return true;
   }
@@ -309,9 +311,11 @@ __global__ void __launch_bounds__(Cfg<H, F8>::kThreads, 1)
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  // The set-up above overlaps the previous kernel; from here on the plan,
+  // The set-up above overlaps the previous kernel; from here on the lengths,
   // the query and the cache it wrote are read.
   pdl_wait();
+  PlanSmem &plan_smem = *reinterpret_cast<PlanSmem *>(sm + C::kOffPlan);
+  const PlanView view = plan_view(a, share, gridDim.x, plan_smem);
 
   if (warp == 0 || (C::kProducers > 1 && warp == C::kProd1Warp)) {
     // ------------------------------------------------------------- producers
@@ -324,7 +328,7 @@ __global__ void __launch_bounds__(Cfg<H, F8>::kThreads, 1)
     const int pid = warp == 0 ? 0 : 1;
     const bool own_rope = pid == C::kProducers - 1;
     Walk w;
-    walk_init(w, a, share);
+    walk_init(w, a, view, share);
     Piece pc;
     RingPos lat, rope, stg;
     int npc = 0;
@@ -477,7 +481,7 @@ __global__ void __launch_bounds__(Cfg<H, F8>::kThreads, 1)
       constexpr uint32_t idS = idesc_bf16(128, H, false, false);
       constexpr uint32_t idO = idesc_bf16(128, H, true, false);
       Walk w;
-      walk_init(w, a, share);
+      walk_init(w, a, view, share);
       Piece pc;
       RingPos lat, rope;   // next slot to consume
       int npc = 0, i = 0;
@@ -591,7 +595,7 @@ __global__ void __launch_bounds__(Cfg<H, F8>::kThreads, 1)
     float *opart = reinterpret_cast<float *>(a.ws + a.L.opart_off);
     float *lse_out = reinterpret_cast<float *>(a.ws + a.L.lse_off);
     Walk w;
-    walk_init(w, a, share);
+    walk_init(w, a, view, share);
     Piece pc;
     int i = 0, npc = 0;
     bool ok = true;
@@ -748,7 +752,7 @@ __global__ void __launch_bounds__(Cfg<H, F8>::kThreads, 1)
     // chunk's unit count are multiples of 32)
     auto has = [&](int rr) { return ct + kCT * rr < kUnitsCh; };
     Walk w;
-    walk_init(w, a, share);
+    walk_init(w, a, view, share);
     Piece pc;
     RingPos stg, lat, rope;
     bool ok = true;
@@ -832,7 +836,7 @@ __global__ void __launch_bounds__(Cfg<H, F8>::kThreads, 1)
 }
 
 template <int H, bool F8>
-cudaError_t launch_h(const AttnArgs &a, int P, cudaStream_t s) {
+cudaError_t launch_h(const AttnArgs &a, int P, cudaStream_t s, const Before &before) {
   using C = Cfg<H, F8>;
   const long long rows = a.page_size ? a.cache_len * kTile : (long long)a.B * a.cache_len;
   if (rows <= 0 || rows >= (1ll << 31) - 256) return cudaErrorNotSupported;
@@ -871,6 +875,7 @@ cudaError_t launch_h(const AttnArgs &a, int P, cudaStream_t s) {
   cudaError_t e = once_per_device(configured, [] {
     return cudaFuncSetAttribute(attn_smallh_kernel<H, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   });
+  if (e == cudaSuccess && before) e = before();
   if (e != cudaSuccess) return e;
   return launch_pdl(attn_smallh_kernel<H, F8>, dim3(P), dim3(C::kThreads), C::kSmem, s, 1, mq, mkv, mkv64, mpair,
                     a, rows);
@@ -878,17 +883,17 @@ cudaError_t launch_h(const AttnArgs &a, int P, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_attn_tc_smallh(const AttnArgs &a, int P, cudaStream_t s) {
+cudaError_t launch_attn_tc_smallh(const AttnArgs &a, int P, cudaStream_t s, const Before &before) {
   if (a.d_c != 512 || a.d_r != 64) return cudaErrorNotSupported;
   if (a.page_size != 0 && a.page_size != kTile) return cudaErrorNotSupported;
   if (a.kv_scale) {
     if (a.n_groups != kGroups8) return cudaErrorNotSupported;
-    if (a.n_h == 16) return launch_h<16, true>(a, P, s);
-    if (a.n_h == 32) return launch_h<32, true>(a, P, s);
+    if (a.n_h == 16) return launch_h<16, true>(a, P, s, before);
+    if (a.n_h == 32) return launch_h<32, true>(a, P, s, before);
     return cudaErrorNotSupported;
   }
-  if (a.n_h == 16) return launch_h<16, false>(a, P, s);
-  if (a.n_h == 32) return launch_h<32, false>(a, P, s);
+  if (a.n_h == 16) return launch_h<16, false>(a, P, s, before);
+  if (a.n_h == 32) return launch_h<32, false>(a, P, s, before);
   return cudaErrorNotSupported;
 }
 

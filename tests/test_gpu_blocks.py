@@ -270,6 +270,15 @@ def test_sparse_split_counts(sh, parts):
     Sparse(sh, (1601, 700), 16, parts, 0).run(parts)
 
 
+@pytest.mark.parametrize("sh", [shape(LITE), shape(V2), shape(V2, n_h=40)])
+@pytest.mark.parametrize("B", [90, 300])
+def test_many_short_sequences(sh, B):
+    """Several ragged sequences to a share, so that one partial last block
+    follows another; more of them than plan sequences that are planned in line."""
+    rng = np.random.default_rng(B)
+    Sparse(sh, [int(n) for n in rng.integers(0, 700, B)], 6, B, 64).run()
+
+
 def test_every_block_selected_is_dense_attention():
     sh = shape(LITE)
     s = Sparse(sh, (640, 333), 10, 1, 64)

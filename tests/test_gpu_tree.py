@@ -71,6 +71,14 @@ def test_lite_lengths_and_sizes(T, page):
     t.check(t.run())
 
 
+@pytest.mark.parametrize("B", [100, 300])
+def test_many_short_sequences(B):
+    """Several trees to a share; more of them than are planned in line."""
+    rng = np.random.default_rng(B)
+    t = Tree(shape(LITE), [int(n) for n in rng.integers(0, 500, B)], 3, B, 64)
+    t.check(t.run())
+
+
 @pytest.mark.parametrize("n_h,T", [(128, 1), (128, 3), (32, 5), (1, 7), (33, 4), (200, 2)])
 def test_head_counts(n_h, T):
     t = Tree(shape(V2, n_h=n_h), (130, 0, 300), T, n_h, 0)
