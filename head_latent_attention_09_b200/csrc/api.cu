@@ -497,15 +497,7 @@ int mla_tree_attn(mla_handle *h, const void *q_abs, const void *cache, long long
     if (tc) {
       // the tensor maps are made before anything is launched
       if (!aligned16(q_abs) || !aligned16(cache) || !aligned16(ctx_lat)) return cudaErrorNotSupported;
-      a.src = src;
-      a.cap = cap;
-      a.inline_plan = a.B <= kInlineSeqs;
-      e = launch_tree_attn_tc_pair(a, t.parts, s, [&] {
-        // the copy comes last: an in-line plan starts beside it
-        cudaError_t b = cudaSuccess;
-        if (!a.inline_plan) b = launch_plan(src, a.B, t.parts, cap, t.tile, a.ws, a.L, a.status, s);
-        return b == cudaSuccess ? launch_tree_copy(src, a, cap, s) : b;
-      });
+      e = launch_tree_attn_tc_pair(a, t.parts, s, [&] { return launch_tree_plan_copy(src, a, t.parts, cap, s); });
     } else {
       e = launch_plan(src, a.B, t.parts, cap, t.tile, a.ws, a.L, a.status, s);
       if (e == cudaSuccess) e = launch_tree_attn_simt(a, t.parts, c.dtype == MLA_FP32, s);

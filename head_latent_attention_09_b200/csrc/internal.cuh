@@ -279,8 +279,8 @@ struct AttnArgs {
   const int *sel = nullptr;
   int sel_k = 0;
   TreeArgs tree;     // B is then the number of plan sequences (runs x batch)
-  // Tensor-core kernels, B <= kInlineSeqs: every CTA makes the plan itself in
-  // shared memory (plan.cuh) from these instead of reading a plan kernel's.
+  // Tensor-core kernels without a tree, B <= kInlineSeqs: every CTA makes the
+  // plan itself in shared memory (plan.cuh) instead of reading a plan kernel's.
   int inline_plan = 0;
   PlanSource src{nullptr};
   long long cap = 0;
@@ -303,9 +303,9 @@ struct AttnArgs {
 cudaError_t launch_plan(const PlanSource &src, int B, int P, long long cap, int tile, char *ws, const WsLayout &L,
                         unsigned *status, cudaStream_t s);
 
-// Tree: the copy of the blocks that hold drafted tokens, for the tensor-core
-// kernel, which starts beside it.
-cudaError_t launch_tree_copy(const PlanSource &src, const AttnArgs &a, long long cap, cudaStream_t s);
+// Tree, for the tensor-core kernel: the plan, and in the same launch the copy
+// of the blocks that hold drafted tokens.
+cudaError_t launch_tree_plan_copy(const PlanSource &src, const AttnArgs &a, int P, long long cap, cudaStream_t s);
 
 // The plan stores two values per plan sequence: the end of its attended tokens
 // (clamped), and its first token (a multiple of kTile), or for selected blocks

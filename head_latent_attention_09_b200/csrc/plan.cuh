@@ -56,18 +56,11 @@ __device__ __forceinline__ void plan_entry(const PlanSource &src, int b, long lo
   *second_out = (int)second;
 }
 
-// Where a kernel finds its plan: in shared memory or in the workspace.
-struct PlanView {
-  const long long *tp, *pb;   // tile prefix and piece base, [B + 1]
-  const int *ends, *seconds;
-  long long P, Ttot;
-  int first;                  // first plan sequence of this share
-};
-
 struct PlanSmem {
   long long tp[kInlineSeqs + 1], pb[kInlineSeqs + 1];
   int ends[kInlineSeqs], seconds[kInlineSeqs];
   long long P, Ttot;
+  int first;   // first plan sequence of this CTA's share
 };
 
 // First plan sequence whose tiles reach past the first tile of share w.
@@ -81,21 +74,9 @@ __device__ __forceinline__ int plan_first(const long long *tp, int B, long long 
   return lo;
 }
 
-// The plan's view for share `share`; with a.inline_plan every thread of the CTA
-// takes part (P_req shares were launched), and block 0 stores the plan.
-__device__ __forceinline__ PlanView plan_view(const AttnArgs &a, int share, int P_req, PlanSmem &o) {
-  PlanView v;
-  if (!a.inline_plan) {
-    const WsHeader *hd = reinterpret_cast<const WsHeader *>(a.ws);
-    v.P = hd->P;
-    v.Ttot = hd->Ttot;
-    v.tp = reinterpret_cast<const long long *>(a.ws + a.L.tile_prefix_off);
-    v.pb = reinterpret_cast<const long long *>(a.ws + a.L.piece_base_off);
-    v.ends = plan_ends(a);
-    v.seconds = plan_seconds(a);
-    v.first = share < v.P ? reinterpret_cast<const int *>(a.ws + a.L.share_first_off)[share] : a.B;
-    return v;
-  }
+// Makes the plan for P_req shares in `o` (every thread of the CTA, which works
+// on share `share`); block 0 stores it in the workspace.
+__device__ __forceinline__ void plan_in_line(const AttnArgs &a, int share, int P_req, PlanSmem &o) {
   const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31;
   for (int b = tid; b < a.B; b += nt) plan_entry(a.src, b, a.cap, a.status, &o.ends[b], &o.seconds[b]);
   __syncthreads();
@@ -143,15 +124,10 @@ __device__ __forceinline__ PlanView plan_view(const AttnArgs &a, int share, int 
       o.P = P;
       o.Ttot = Ttot;
     }
+    __syncwarp();
+    if (lane == 0 && share < P) o.first = plan_first(o.tp, a.B, share, P, Ttot);
   }
   __syncthreads();
-  v.tp = o.tp;
-  v.pb = o.pb;
-  v.ends = o.ends;
-  v.seconds = o.seconds;
-  v.P = o.P;
-  v.Ttot = o.Ttot;
-  v.first = share < v.P ? plan_first(o.tp, a.B, share, v.P, v.Ttot) : a.B;
   if (blockIdx.x == 0) {
     long long *tp = reinterpret_cast<long long *>(a.ws + a.L.tile_prefix_off);
     long long *pb = reinterpret_cast<long long *>(a.ws + a.L.piece_base_off);
@@ -164,16 +140,15 @@ __device__ __forceinline__ PlanView plan_view(const AttnArgs &a, int share, int 
         ends[a.B + b] = o.seconds[b];
       }
     }
-    for (int w = tid; w < v.P; w += nt) first[w] = plan_first(o.tp, a.B, w, v.P, v.Ttot);
+    for (int w = tid; w < o.P; w += nt) first[w] = plan_first(o.tp, a.B, w, o.P, o.Ttot);
     if (tid == 0) {
       WsHeader *hd = reinterpret_cast<WsHeader *>(a.ws);
       hd->B = a.B;
-      hd->P = v.P;
-      hd->Ttot = v.Ttot;
+      hd->P = o.P;
+      hd->Ttot = o.Ttot;
       hd->n_pieces = o.pb[a.B];
     }
   }
-  return v;
 }
 
 }  // namespace mla

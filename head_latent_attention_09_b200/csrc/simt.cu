@@ -164,16 +164,20 @@ __device__ __forceinline__ uint4 finite_or_zero(uint4 v) {
   return make_uint4(one(v.x), one(v.y), one(v.z), one(v.w));
 }
 
-// Tree: the copy of the blocks that hold drafted tokens, kCopyBlocks blocks of
-// kCopyRows rows per sequence (rows of 72 16-byte units).  The attention kernel
-// starts while this one runs, and waits for it only before it reads a copied
-// block; it may start as soon as the kernels before this one are done, hence
-// the trigger behind the wait.
+// Tree: block 0 makes the plan while the others copy the blocks that hold
+// drafted tokens, kCopyBlocks blocks of kCopyRows rows per sequence (rows of
+// 72 16-byte units).  (The plan made in line, with the attention kernel waiting
+// for the copy only where it reads it, saved 0.7 us of 25 on one short sequence
+// and cost 2 % on long ones, whose kernel then spilled registers.)
 constexpr int kCopyRows = 8, kCopyBlocks = kTreeCopyRows / kCopyRows;
-__global__ void __launch_bounds__(288) tree_copy_kernel(PlanSource src, AttnArgs a, long long cap) {
-  pdl_wait();
+__global__ void __launch_bounds__(1024) tree_plan_copy_kernel(PlanSource src, AttnArgs a, int P_req, long long cap) {
   pdl_trigger();
-  const int b = blockIdx.x / kCopyBlocks, r0 = blockIdx.x % kCopyBlocks * kCopyRows;
+  pdl_wait();
+  if (blockIdx.x == 0) {
+    make_plan(src, a.B, P_req, cap, a.plan_tile, a.ws, a.L, a.status);
+    return;
+  }
+  const int b = (blockIdx.x - 1) / kCopyBlocks, r0 = (blockIdx.x - 1) % kCopyBlocks * kCopyRows;
   const long long cached = min(max((long long)src.ctx_len[b], 0ll), cap);
   const long long end = min(cached + src.drafted, cap);
   const long long first = cached / kTile * kTile;
@@ -596,10 +600,11 @@ cudaError_t launch_plan(const PlanSource &src, int B, int P, long long cap, int 
   return launch_pdl(plan_kernel, dim3(1), dim3(threads), 0, s, 1, src, B, P, cap, tile, ws, L, status);
 }
 
-cudaError_t launch_tree_copy(const PlanSource &src, const AttnArgs &a, long long cap, cudaStream_t s) {
-  const long long blocks = (long long)(a.B / src.runs) * kCopyBlocks;
+cudaError_t launch_tree_plan_copy(const PlanSource &src, const AttnArgs &a, int P, long long cap, cudaStream_t s) {
+  const long long blocks = 1 + (long long)(a.B / src.runs) * kCopyBlocks;
   if (a.d_c + a.d_r != 576 || src.drafted > kTreeMaxDrafted || blocks > 0x7fffffffLL) return cudaErrorNotSupported;
-  return launch_pdl(tree_copy_kernel, dim3((unsigned)blocks), dim3(288), 0, s, 1, src, a, cap);
+  const int threads = a.B >= 1024 ? 1024 : (a.B <= 288 ? 288 : (a.B + 31) / 32 * 32);
+  return launch_pdl(tree_plan_copy_kernel, dim3((unsigned)blocks), dim3(threads), 0, s, 1, src, a, P, cap);
 }
 
 cudaError_t launch_attn_simt(const AttnArgs &a, int P, bool fp32, cudaStream_t s) {

@@ -53,6 +53,8 @@
 // kernel winds down without further waits.
 #include <math_constants.h>
 
+#include <type_traits>
+
 #include "plan.cuh"
 #include "ptx.cuh"
 
@@ -118,49 +120,65 @@ struct Piece {
   int ntiles;          // 256-token MMA tiles
 };
 
+// A role's position in its share.  The plan lies in shared memory (kInl) or in
+// the workspace; either way its arrays are found again at every use, so that
+// they take no registers through the loops.
+template <bool kInl>
 struct Walk {
-  const long long *tp;
-  const long long *pb;
-  const int *ends, *seconds;
-  long long P, Ttot, t0, t1;
+  const PlanSmem *o;
+  long long t0, t1;
   int b;
-  int B;
   int member;   // tree: which of the share's workers this is
 };
+template <bool kInl>
+__device__ __forceinline__ const long long *plan_tp(const AttnArgs &a, const Walk<kInl> &w) {
+  return kInl ? w.o->tp : reinterpret_cast<const long long *>(a.ws + a.L.tile_prefix_off);
+}
+template <bool kInl>
+__device__ __forceinline__ const long long *plan_pb(const AttnArgs &a, const Walk<kInl> &w) {
+  return kInl ? w.o->pb : reinterpret_cast<const long long *>(a.ws + a.L.piece_base_off);
+}
+template <bool kInl>
+__device__ __forceinline__ long long plan_P(const AttnArgs &a, const Walk<kInl> &w) {
+  return kInl ? w.o->P : reinterpret_cast<const WsHeader *>(a.ws)->P;
+}
+template <bool kInl>
+__device__ __forceinline__ long long plan_Ttot(const AttnArgs &a, const Walk<kInl> &w) {
+  return kInl ? w.o->Ttot : reinterpret_cast<const WsHeader *>(a.ws)->Ttot;
+}
 
-__device__ __forceinline__ void walk_init(Walk &w, const AttnArgs &a, const PlanView &v, int share) {
-  w.P = v.P;
-  w.Ttot = v.Ttot;
-  w.tp = v.tp;
-  w.pb = v.pb;
-  w.ends = v.ends;
-  w.seconds = v.seconds;
-  w.B = a.B;
+template <bool kInl>
+__device__ __forceinline__ void walk_init(Walk<kInl> &w, const AttnArgs &a, const PlanSmem &o, int share) {
+  w.o = &o;
   w.member = (blockIdx.x >> 1) % a.tree.gang;
-  w.b = v.first;
-  if (share >= w.P) return;
-  w.t0 = plan_begin(share, w.P, w.Ttot);
-  w.t1 = plan_begin(share + 1, w.P, w.Ttot);
+  const long long P = plan_P(a, w), Ttot = plan_Ttot(a, w);
+  w.b = a.B;
+  if (share >= P) return;
+  w.b = kInl ? o.first : reinterpret_cast<const int *>(a.ws + a.L.share_first_off)[share];
+  w.t0 = plan_begin(share, P, Ttot);
+  w.t1 = plan_begin(share + 1, P, Ttot);
 }
 
 // Next piece of this share; false when done.
-template <bool kTree>
-__device__ __forceinline__ bool walk_next(Walk &w, const AttnArgs &a, int share, Piece &pc) {
-  while (w.b < w.B && w.tp[w.b] < w.t1) {
+template <bool kTree, bool kInl>
+__device__ __forceinline__ bool walk_next(Walk<kInl> &w, const AttnArgs &a, int share, Piece &pc) {
+  const long long *tp = plan_tp(a, w);
+  const int *ends = kInl ? w.o->ends : plan_ends(a), *seconds = kInl ? w.o->seconds : plan_seconds(a);
+  while (w.b < a.B && tp[w.b] < w.t1) {
     const int b = w.b++;
-    const long long s0 = w.t0 > w.tp[b] ? w.t0 : w.tp[b];
-    const long long s1 = w.t1 < w.tp[b + 1] ? w.t1 : w.tp[b + 1];
+    const long long s0 = w.t0 > tp[b] ? w.t0 : tp[b];
+    const long long s1 = w.t1 < tp[b + 1] ? w.t1 : tp[b + 1];
     if (s0 >= s1) continue;
     pc.b = kTree ? b / a.tree.runs : b;
     pc.v = b;
     pc.g = kTree ? (b - pc.b * a.tree.runs) * a.tree.gang + w.member : 0;
     if (kTree && pc.g >= a.tree.groups) continue;
-    const int ctx = w.ends[b];
-    const int beg = kTree || a.sel ? 0 : w.seconds[b];
-    pc.cached = kTree || a.sel ? w.seconds[b] : ctx;
-    pc.piece = w.pb[b] + (share - plan_share_of_tile(w.tp[b], w.P, w.Ttot));
-    pc.tok_begin = beg + (int)((s0 - w.tp[b]) * a.plan_tile);
-    const long long e = beg + (s1 - w.tp[b]) * a.plan_tile;
+    const int ctx = ends[b];
+    const int beg = kTree || a.sel ? 0 : seconds[b];
+    pc.cached = kTree || a.sel ? seconds[b] : ctx;
+    pc.piece = kTree ? 0 : plan_pb(a, w)[b] + (share - plan_share_of_tile(tp[b], plan_P(a, w), plan_Ttot(a, w)));
+    pc.tok_begin = beg + (int)((s0 - tp[b]) * a.plan_tile);
+    const long long e = beg + (s1 - tp[b]) * a.plan_tile;
     pc.tok_end = (int)(e < ctx ? e : ctx);
     pc.ctx = ctx;
     pc.ntiles = (pc.tok_end - pc.tok_begin + kTileTok - 1) / kTileTok;
@@ -262,7 +280,7 @@ __device__ __forceinline__ int tile_subs(const Piece &p, int t0) {
   return (n + kSubTok - 1) / kSubTok;
 }
 
-template <bool kTree>
+template <bool kTree, bool kInl>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     attn_pair_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
                      const __grid_constant__ CUtensorMap mapV, const __grid_constant__ CUtensorMap mapV2,
@@ -314,13 +332,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   // The set-up above overlaps the previous kernel; from here on the lengths,
-  // the query and the cache it wrote are read.  A tree that plans in line runs
-  // behind the copy of its last blocks, which starts it once the kernels before
-  // that copy are done: only the copied blocks are waited for, by the producer.
-  const bool late_wait = kTree && a.inline_plan;
-  if (!late_wait) pdl_wait();
+  // the query and the cache it wrote are read.
+  pdl_wait();
   PlanSmem &plan_smem = *reinterpret_cast<PlanSmem *>(sm + kOffPlan);
-  const PlanView view = plan_view(a, share, kTree ? gridDim.x / (2 * a.tree.gang) : gridDim.x / 2, plan_smem);
+  if (kInl) plan_in_line(a, share, gridDim.x / 2, plan_smem);
 
   if (warp == 0) {
     // --------------------------------------------------------------- producer
@@ -342,8 +357,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       ptx::tma_prefetch_desc(&mapV);
       ptx::tma_prefetch_desc(&mapV2);
       if (kTree) ptx::tma_prefetch_desc(&mapT);
-      Walk w;
-      walk_init(w, a, view, share);
+      Walk<kInl> w;
+      walk_init(w, a, plan_smem, share);
       const uint64_t last_read = ptx::l2_policy_evict_first();
       int slot = 0;              // ring slot of the next job
       uint32_t phase = 1;        // parity of its empty barrier to wait for (the first round passes at once)
@@ -363,14 +378,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // V sub-stages of the tile at token t0 of piece p: tokens t0 + 64t..,
       // latent columns 256g + 128 * rank .. +128, one 3D box: 64 rows x both
       // 64-column chunks.
-      bool waited = !late_wait;
       int nend = 0;              // partial blocks so far
       auto issue_v = [&](const Piece &p, int t0, const Rows &x) -> bool {
         const int nsub = tile_subs(p, t0);
-        if (kTree && !waited && t0 + kTileTok > p.cached) {
-          pdl_wait();   // the copy is complete
-          waited = true;
-        }
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
           if (t >= nsub) break;
@@ -408,7 +418,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       Rows x, vx;
       int vt0 = 0, npc = 0;
       bool vpending = false, ok = true;
-      while (ok && walk_next<kTree>(w, a, share, pc)) {
+      while (ok && walk_next<kTree, kInl>(w, a, share, pc)) {
         if (npc > 0 && !ptx::mbar_wait(bars.qempty(), (npc - 1) & 1, a.status, abort_flag)) break;
         if (leader) ptx::mbar_arrive_expect_tx(bars.qfull(), 2 * kQBytes);
         for (int c = 0; c < 9; ++c) {
@@ -456,12 +466,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // sequence, so that no unwritten cache row (possibly NaN) reaches P.V.
     if (!kTree) {
       const uint32_t lf0 = ptx::leader_addr(bars.full(0));
-      Walk w;
-      walk_init(w, a, view, share);
+      Walk<kInl> w;
+      walk_init(w, a, plan_smem, share);
       Piece pc;
       int n = 0;
       bool ok = true;
-      while (ok && walk_next<kTree>(w, a, share, pc)) {
+      while (ok && walk_next<kTree, kInl>(w, a, share, pc)) {
         const int row0 = pc.ctx % kSubTok;
         if (pc.tok_end != pc.ctx || row0 == 0) continue;
         for (int g = 0; g < 2; ++g) {
@@ -482,8 +492,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ MMA issue
     const bool issuer = ptx::elect_one();
     if (leader && issuer) {
-      Walk w;
-      walk_init(w, a, view, share);
+      Walk<kInl> w;
+      walk_init(w, a, plan_smem, share);
       Piece pc;
       int npc = 0, i = 0;
       int rs = 0;                 // ring slot of the next job
@@ -538,7 +548,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ptx::mma_commit_pair_both(bars.odone(t.i & 1));
         return true;
       };
-      while (ok && walk_next<kTree>(w, a, share, pc)) {
+      while (ok && walk_next<kTree, kInl>(w, a, share, pc)) {
         if (!ptx::mbar_wait(bars.qfull(), npc & 1, a.status, abort_flag)) { ok = false; break; }
         for (int k = 0; k < pc.ntiles && ok; ++k) {
           const uint32_t dS = tmem + (i & 1) * kColS;
@@ -585,12 +595,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     float *opart = reinterpret_cast<float *>(a.ws + a.L.opart_off);
     float *lse_out = reinterpret_cast<float *>(a.ws + a.L.lse_off);
     uint8_t *prow = sP + part * 8192 + h * 128;   // this row of the thread's 64-token P chunk
-    Walk w;
-    walk_init(w, a, view, share);
+    Walk<kInl> w;
+    walk_init(w, a, plan_smem, share);
     Piece pc;
     int i = 0, npc_s = 0;
     bool ok = true;
-    while (ok && walk_next<kTree>(w, a, share, pc)) {
+    while (ok && walk_next<kTree, kInl>(w, a, share, pc)) {
       float m_run = -CUDART_INF_F, l_part = 0.f;
       // tree: this thread's query row of the sequence, and its drafted tokens
       const int row = 128 * pc.g + 64 * (int)rank + h;
@@ -712,7 +722,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       long long slot = pc.piece;
       bool whole = false;
       if (kTree) {
-        const TreePiece t = tree_piece(a, w.tp, pc.v, share, w.member, w.P, w.Ttot);
+        const TreePiece t = tree_piece(a, plan_tp(a, w), pc.v, share, w.member, plan_P(a, w), plan_Ttot(a, w));
         whole = t.whole;
         slot = t.slot;
       }
@@ -787,7 +797,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
 
   // ---------------------------------------------------------------- teardown
-  if (late_wait) pdl_wait();   // what follows this kernel may rely on the copy's being done too
   ptx::tc_fence_before();
   __syncwarp();
   ptx::cluster_sync_all();
@@ -830,14 +839,20 @@ cudaError_t launch_pair(const AttnArgs &a, int P, cudaStream_t s, const Before &
   const uint64_t dt3[3] = {64, (uint64_t)batch * kTreeCopyRows, 9};
   if (kTree && !encode_map_bf16(&mt, a.ws + a.tree.copy_off, 3, dt3, st3, boxv3, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorNotSupported;
-  static std::atomic<int> configured[kMaxDevices];
-  cudaError_t e = once_per_device(configured, [] {
-    return cudaFuncSetAttribute(attn_pair_kernel<kTree>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemAlloc);
-  });
-  if (e == cudaSuccess && before) e = before();
-  if (e != cudaSuccess) return e;
-  return launch_pdl(attn_pair_kernel<kTree>, dim3(2 * P * a.tree.gang), dim3(kThreads), kSmemAlloc, s, 1, mq, mk, mv, mv2, mt, a,
-                    rows);
+  auto go = [&](auto inl) {
+    constexpr bool kInl = decltype(inl)::value;
+    static std::atomic<int> configured[kMaxDevices];
+    cudaError_t e = once_per_device(configured, [] {
+      return cudaFuncSetAttribute(attn_pair_kernel<kTree, kInl>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemAlloc);
+    });
+    if (e == cudaSuccess && before) e = before();
+    if (e != cudaSuccess) return e;
+    return launch_pdl(attn_pair_kernel<kTree, kInl>, dim3(2 * P * a.tree.gang), dim3(kThreads), kSmemAlloc, s, 1, mq, mk,
+                      mv, mv2, mt, a, rows);
+  };
+  if constexpr (!kTree)
+    if (a.inline_plan) return go(std::true_type());
+  return go(std::false_type());
 }
 }  // namespace
 

@@ -144,16 +144,29 @@ struct Walk {
   int b, B;
 };
 
-__device__ __forceinline__ void walk_init(Walk &w, const AttnArgs &a, const PlanView &v, int share) {
-  w.P = v.P;
-  w.Ttot = v.Ttot;
-  w.tp = v.tp;
-  w.pb = v.pb;
-  w.ends = v.ends;
-  w.seconds = v.seconds;
+__device__ __forceinline__ void walk_init(Walk &w, const AttnArgs &a, const PlanSmem &o, int share) {
   w.B = a.B;
-  w.b = v.first;
-  if (share >= w.P) return;
+  w.b = a.B;
+  if (a.inline_plan) {
+    w.P = o.P;
+    w.Ttot = o.Ttot;
+    w.tp = o.tp;
+    w.pb = o.pb;
+    w.ends = o.ends;
+    w.seconds = o.seconds;
+    if (share >= w.P) return;
+    w.b = o.first;
+  } else {
+    const WsHeader *hd = reinterpret_cast<const WsHeader *>(a.ws);
+    w.P = hd->P;
+    w.Ttot = hd->Ttot;
+    w.tp = reinterpret_cast<const long long *>(a.ws + a.L.tile_prefix_off);
+    w.pb = reinterpret_cast<const long long *>(a.ws + a.L.piece_base_off);
+    w.ends = plan_ends(a);
+    w.seconds = plan_seconds(a);
+    if (share >= w.P) return;
+    w.b = reinterpret_cast<const int *>(a.ws + a.L.share_first_off)[share];   // found by the plan
+  }
   w.t0 = plan_begin(share, w.P, w.Ttot);
   w.t1 = plan_begin(share + 1, w.P, w.Ttot);
 }
@@ -315,7 +328,7 @@ __global__ void __launch_bounds__(Cfg<H, F8>::kThreads, 1)
   // the query and the cache it wrote are read.
   pdl_wait();
   PlanSmem &plan_smem = *reinterpret_cast<PlanSmem *>(sm + C::kOffPlan);
-  const PlanView view = plan_view(a, share, gridDim.x, plan_smem);
+  if (a.inline_plan) plan_in_line(a, share, gridDim.x, plan_smem);
 
   if (warp == 0 || (C::kProducers > 1 && warp == C::kProd1Warp)) {
     // ------------------------------------------------------------- producers
@@ -328,7 +341,7 @@ __global__ void __launch_bounds__(Cfg<H, F8>::kThreads, 1)
     const int pid = warp == 0 ? 0 : 1;
     const bool own_rope = pid == C::kProducers - 1;
     Walk w;
-    walk_init(w, a, view, share);
+    walk_init(w, a, plan_smem, share);
     Piece pc;
     RingPos lat, rope, stg;
     int npc = 0;
@@ -481,7 +494,7 @@ __global__ void __launch_bounds__(Cfg<H, F8>::kThreads, 1)
       constexpr uint32_t idS = idesc_bf16(128, H, false, false);
       constexpr uint32_t idO = idesc_bf16(128, H, true, false);
       Walk w;
-      walk_init(w, a, view, share);
+      walk_init(w, a, plan_smem, share);
       Piece pc;
       RingPos lat, rope;   // next slot to consume
       int npc = 0, i = 0;
@@ -595,7 +608,7 @@ __global__ void __launch_bounds__(Cfg<H, F8>::kThreads, 1)
     float *opart = reinterpret_cast<float *>(a.ws + a.L.opart_off);
     float *lse_out = reinterpret_cast<float *>(a.ws + a.L.lse_off);
     Walk w;
-    walk_init(w, a, view, share);
+    walk_init(w, a, plan_smem, share);
     Piece pc;
     int i = 0, npc = 0;
     bool ok = true;
@@ -752,7 +765,7 @@ __global__ void __launch_bounds__(Cfg<H, F8>::kThreads, 1)
     // chunk's unit count are multiples of 32)
     auto has = [&](int rr) { return ct + kCT * rr < kUnitsCh; };
     Walk w;
-    walk_init(w, a, view, share);
+    walk_init(w, a, plan_smem, share);
     Piece pc;
     RingPos stg, lat, rope;
     bool ok = true;
