@@ -653,11 +653,12 @@ __device__ __forceinline__ void store4<__nv_bfloat16>(__nv_bfloat16 *dst, float4
 
 constexpr int kMergeAhead = 8;
 template <typename T, int kPer>   // float4 columns of a lane: 4 (one warp a row) or 1 (four warps a row)
-__global__ void __launch_bounds__(256) combine_vec_kernel(const char *ws, WsLayout L, int B, int n_h, int d_c,
-                                                          T *ctx_lat, float *lse_out) {
+__global__ void __launch_bounds__(256, 4) combine_vec_kernel(const char *ws, WsLayout L, int B, int n_h, int d_c,
+                                                             T *ctx_lat, float *lse_out) {
   pdl_trigger();
   pdl_wait();
   constexpr int kSegs = 4 / kPer;
+  constexpr int kAhead = kMergeAhead / kPer;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long unit = (long long)blockIdx.x * 8 + warp;
   const long long row = unit / kSegs;   // = b * n_h + h
@@ -665,15 +666,29 @@ __global__ void __launch_bounds__(256) combine_vec_kernel(const char *ws, WsLayo
   if (row >= (long long)B * n_h) return;
   const int b = (int)(row / n_h), h = (int)(row % n_h);
   const long long *pb = reinterpret_cast<const long long *>(ws + L.piece_base_off);
-  const float *lse = reinterpret_cast<const float *>(ws + L.lse_off);
-  const float *op = reinterpret_cast<const float *>(ws + L.opart_off);
-  const long long p0 = pb[b], p1 = pb[b + 1];
-  float m = -CUDART_INF_F;
-  for (long long p = p0 + lane; p < p1; p += 32) m = fmaxf(m, lse[part_row(L, p, h)]);
+  const float *lse = reinterpret_cast<const float *>(ws + L.lse_off) + part_row(L, pb[b], h);
+  const int n = (int)(pb[b + 1] - pb[b]);   // the row's pieces are consecutive
+  const int n4 = d_c / 4;
+  const float4 *src = reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(ws + L.opart_off) +
+                                                       part_row(L, pb[b], h) * (long long)d_c) + f0;
+  // Partials j0 .. of the row; the first batch is requested before the weights
+  // are known.
+  float4 v[kAhead][kPer];
+  auto request = [&](int j0) {
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        v[j][i] = j0 + j < n && f0 + 32 * i < n4 ? __ldg(src + (long long)(j0 + j) * n4 + 32 * i)
+                                                 : make_float4(0.f, 0.f, 0.f, 0.f);
+  };
+  request(0);
+  const float l0 = lane < n ? lse[lane] : -CUDART_INF_F;
+  float m = l0;
+  for (int p = 32 + lane; p < n; p += 32) m = fmaxf(m, lse[p]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   T *dst = ctx_lat + row * d_c;
-  const int n4 = d_c / 4;
   if (m == -CUDART_INF_F) {
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
@@ -681,37 +696,29 @@ __global__ void __launch_bounds__(256) combine_vec_kernel(const char *ws, WsLayo
     if (lse_out && f0 == 0) lse_out[row] = -CUDART_INF_F;
     return;
   }
-  float tot = 0.f;
-  for (long long p = p0 + lane; p < p1; p += 32) tot += expf(lse[part_row(L, p, h)] - m);
+  float tot = lane < n ? expf(l0 - m) : 0.f;
+  for (int p = 32 + lane; p < n; p += 32) tot += expf(lse[p] - m);
   tot = warp_sum(tot);
   const float inv = 1.f / tot;
   float4 acc[kPer];
 #pragma unroll
   for (int i = 0; i < kPer; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-  constexpr int kAhead = kPer == 1 ? kMergeAhead : kMergeAhead / 2;
-  for (long long q0 = p0; q0 < p1; q0 += 32) {
-    const int n = (int)min(32ll, p1 - q0);
-    const float wl = lane < n ? expf(lse[part_row(L, q0 + lane, h)] - m) * inv : 0.f;
-    for (int j0 = 0; j0 < n; j0 += kAhead) {
-      float4 v[kAhead][kPer];
+  float wl = lane < n ? expf(l0 - m) * inv : 0.f;
+  for (int j0 = 0; j0 < n; j0 += kAhead) {
+    if (j0 > 0) {
+      request(j0);
+      if ((j0 & 31) == 0) wl = j0 + lane < n ? expf(lse[j0 + lane] - m) * inv : 0.f;
+    }
 #pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
-        const float4 *src = reinterpret_cast<const float4 *>(op + part_row(L, q0 + j0 + j, h) * (long long)d_c);
+    for (int j = 0; j < kAhead; ++j) {
+      const float w = __shfl_sync(0xffffffffu, wl, (j0 + j) & 31);
+      if (j0 + j >= n) continue;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i)
-          v[j][i] = j0 + j < n && f0 + 32 * i < n4 ? __ldg(src + f0 + 32 * i) : make_float4(0.f, 0.f, 0.f, 0.f);
-      }
-#pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
-        const float w = __shfl_sync(0xffffffffu, wl, (j0 + j) & 31);
-        if (j0 + j >= n) continue;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          acc[i].x += w * v[j][i].x;
-          acc[i].y += w * v[j][i].y;
-          acc[i].z += w * v[j][i].z;
-          acc[i].w += w * v[j][i].w;
-        }
+      for (int i = 0; i < kPer; ++i) {
+        acc[i].x += w * v[j][i].x;
+        acc[i].y += w * v[j][i].y;
+        acc[i].z += w * v[j][i].z;
+        acc[i].w += w * v[j][i].w;
       }
     }
   }
