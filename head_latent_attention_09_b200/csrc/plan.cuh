@@ -78,12 +78,17 @@ __device__ __forceinline__ int plan_first(const long long *tp, int B, long long 
 // on share `share`); block 0 stores it in the workspace.
 __device__ __forceinline__ void plan_in_line(const AttnArgs &a, int share, int P_req, PlanSmem &o) {
   const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31;
-  for (int b = tid; b < a.B; b += nt) plan_entry(a.src, b, a.cap, a.status, &o.ends[b], &o.seconds[b]);
+  const bool from0 = plan_from0(a.src);
+  for (int b = tid; b < a.B; b += nt) {
+    int end, second;
+    plan_entry(a.src, b, a.cap, a.status, &end, &second);
+    o.ends[b] = end;
+    o.seconds[b] = second;
+    o.pb[b] = ((unsigned)(end - (from0 ? 0 : second)) + (unsigned)a.plan_tile - 1u) / (unsigned)a.plan_tile;   // tiles
+  }
   __syncthreads();
   if (tid < 32) {
     const int per = (a.B + 31) / 32, b0 = min(a.B, lane * per), b1 = min(a.B, b0 + per);
-    const bool from0 = plan_from0(a.src);
-    auto tiles = [&](int b) { return ceil_div_ll(o.ends[b] - (from0 ? 0 : o.seconds[b]), a.plan_tile); };
     auto before = [&](long long x, long long *total) {   // exclusive prefix over the lanes
       long long s = x;
 #pragma unroll
@@ -95,20 +100,18 @@ __device__ __forceinline__ void plan_in_line(const AttnArgs &a, int share, int P
       return s - x;
     };
     long long sum = 0, Ttot, pieces;
-    for (int b = b0; b < b1; ++b) sum += tiles(b);
+    for (int b = b0; b < b1; ++b) sum += o.pb[b];
     long long run = before(sum, &Ttot);
     for (int b = b0; b < b1; ++b) {
       o.tp[b] = run;
-      run += tiles(b);
+      run += o.pb[b];
     }
     const long long P = Ttot < (long long)P_req ? Ttot : (long long)P_req;
-    auto pieces_of = [&](int b) -> long long {
-      const long long t = tiles(b);
-      return t > 0 ? plan_share_of_tile(o.tp[b] + t - 1, P, Ttot) - plan_share_of_tile(o.tp[b], P, Ttot) + 1 : 0;
-    };
     long long np = 0;
     for (int b = b0; b < b1; ++b) {
-      const long long n = pieces_of(b);
+      const long long t = o.pb[b];
+      const long long n =
+          t > 0 ? plan_share_of_tile(o.tp[b] + t - 1, P, Ttot) - plan_share_of_tile(o.tp[b], P, Ttot) + 1 : 0;
       o.pb[b] = n;
       np += n;
     }

@@ -24,7 +24,9 @@
 // while the softmax runs.
 //
 // Per-head softmax statistics are reductions across tokens, i.e. across
-// threads: warp shuffles over 32 lanes, then shared memory across the warps.
+// threads: a transposing reduction over the 32 lanes (lane l ends with head l's
+// value), then shared memory across the warps; a head's running maximum and sum
+// live in its lane and reach the others by shuffles.
 //
 // Warp roles: warps 0 and 6 TMA producers (bf16; FP8 has warp 0 only), warp 1
 // tensor-memory allocation and MMA issue, warps 2-5 softmax / rescale /
@@ -216,6 +218,27 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, unsign
   if (ok && (threadIdx.x & 31) != 0) ptx::mbar_test_wait(bar, parity);
   __syncwarp();
   return ok;
+}
+
+// Reduces H (16 or 32) values per lane over the warp's lanes, each value on its
+// own: every exchange halves the values a lane is in charge of, so that lane l
+// ends with value l mod H (16 or 31 shuffles where a butterfly per value takes
+// 5 H; the epilogue's and the maximum's unrolled butterflies also cost
+// microseconds of instruction fetch on a piece of one tile).
+template <int H, typename Op>
+__device__ __forceinline__ float over_lanes(float (&x)[H], Op op) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = H / 2; o > 0; o >>= 1) {
+    const bool up = (lane & o) != 0;
+#pragma unroll
+    for (int j = 0; j < o; ++j) {
+      const float give = up ? x[j] : x[j + o], keep = up ? x[j + o] : x[j];
+      x[j] = op(keep, __shfl_xor_sync(0xffffffffu, give, o));
+    }
+  }
+  if (H == 16) x[0] = op(x[0], __shfl_xor_sync(0xffffffffu, x[0], 16));
+  return x[0];
 }
 
 // A ring of slots consumed in fill order: slot and phase parity of the next use.
@@ -613,55 +636,47 @@ __global__ void __launch_bounds__(Cfg<H, F8>::kThreads, 1)
     int i = 0, npc = 0;
     bool ok = true;
     while (ok && walk_next(w, a, share, pc)) {
-      float m_run[H], l_part[H];
+      // Per-head state lives in the lane of that head (lane mod H): the running
+      // maximum here, the sum and its reciprocal at the end; l_part[hh] is this
+      // token row's own share of head hh's sum.
+      const int hl = lane & (H - 1);
+      float m_run = -CUDART_INF_F, l_part[H];
 #pragma unroll
-      for (int hh = 0; hh < H; ++hh) {
-        m_run[hh] = -CUDART_INF_F;
-        l_part[hh] = 0.f;
-      }
+      for (int hh = 0; hh < H; ++hh) l_part[hh] = 0.f;
       for (int k = 0; k < pc.ntiles; ++k, ++i) {
         const int tok = pc.tok_begin + kTileTok * k + row;
         const bool valid = tok < pc.tok_end;
         if (!warp_wait(bar + C::bSFull + (i & 1), (i >> 1) & 1, a.status, abort_flag)) { ok = false; break; }
         ptx::tc_fence_after();
-        float s[H];
+        float s[H], x[H];
 #pragma unroll
         for (int c = 0; c < H / 16; ++c) {
           uint32_t r[16];
           ptx::tmem_ld16(lane_addr + (i & 1) * H + 16 * c, r);
           ptx::tmem_ld_wait();
 #pragma unroll
-          for (int j = 0; j < 16; ++j) s[16 * c + j] = valid ? __uint_as_float(r[j]) * a.scale_log2 : -CUDART_INF_F;
+          for (int j = 0; j < 16; ++j) x[16 * c + j] = s[16 * c + j] = valid ? __uint_as_float(r[j]) : -CUDART_INF_F;
         }
         // per-head maximum over the tile's 128 tokens: 32 lanes, then 4 warps
         float *rm = red_m + (i & 1) * 4 * H;
-#pragma unroll
-        for (int hh = 0; hh < H; ++hh) {
-          float v = s[hh];
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-          if (lane == (hh & 31)) rm[q * H + hh] = v;
-        }
+        const float mw = over_lanes<H>(x, [](float u, float v) { return fmaxf(u, v); });
+        if (lane < H) rm[q * H + lane] = mw;
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(bar + C::bXchg + (i & 1));
         if (!warp_wait(bar + C::bXchg + (i & 1), (i >> 1) & 1, a.status, abort_flag)) { ok = false; break; }
-        bool any_rescale = false;
-        float alpha[H];
+        const float mt = fmaxf(fmaxf(rm[hl], rm[H + hl]), fmaxf(rm[2 * H + hl], rm[3 * H + hl])) * a.scale_log2;
+        const bool grows = mt > m_run + kRescale;
+        const float alpha = grows ? exp2f(m_run - mt) : 1.f;
+        if (grows) m_run = mt;
+        const bool any_grows = __any_sync(0xffffffffu, grows);
+        if (any_grows) {
 #pragma unroll
-        for (int hh = 0; hh < H; ++hh) {
-          const float mt = fmaxf(fmaxf(rm[hh], rm[H + hh]), fmaxf(rm[2 * H + hh], rm[3 * H + hh]));
-          alpha[hh] = 1.f;
-          if (mt > m_run[hh] + kRescale) {
-            alpha[hh] = exp2f(m_run[hh] - mt);
-            any_rescale |= k > 0;
-            m_run[hh] = mt;
-            l_part[hh] *= alpha[hh];
-          }
+          for (int hh = 0; hh < H; ++hh) l_part[hh] *= __shfl_sync(0xffffffffu, alpha, hh);
         }
         float p[H];
 #pragma unroll
         for (int hh = 0; hh < H; ++hh) {
-          p[hh] = ptx::exp2_approx(s[hh] - m_run[hh]);
+          p[hh] = ptx::exp2_approx(fmaf(s[hh], a.scale_log2, -__shfl_sync(0xffffffffu, m_run, hh)));
           l_part[hh] += p[hh];
         }
         if (i >= 2 && !warp_wait(bar + C::bPFree + (i & 1), ((i >> 1) - 1) & 1, a.status, abort_flag)) {
@@ -678,7 +693,7 @@ __global__ void __launch_bounds__(Cfg<H, F8>::kThreads, 1)
             *reinterpret_cast<__nv_bfloat16 *>(pt + hh * 128 + ((unit ^ (hh & 7)) << 4) + inunit) =
                 __float2bfloat16_rn(p[hh]);
         }
-        if (__any_sync(0xffffffffu, any_rescale)) {
+        if (any_grows && k > 0) {
           // P.V of the previous tile must be complete before O^T is rescaled
           // (o_done[(i-1)&1] completes with it; nothing later is issued before
           // this tile's P is full).
@@ -695,7 +710,8 @@ __global__ void __launch_bounds__(Cfg<H, F8>::kThreads, 1)
               ptx::tmem_ld16(lane_addr + C::kColO + f * H + 16 * c, r);
               ptx::tmem_ld_wait();
 #pragma unroll
-              for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * alpha[16 * c + j]);
+              for (int j = 0; j < 16; ++j)
+                r[j] = __float_as_uint(__uint_as_float(r[j]) * __shfl_sync(0xffffffffu, alpha, 16 * c + j));
               ptx::tmem_st16(lane_addr + C::kColO + f * H + 16 * c, r);
             }
           }
@@ -708,38 +724,30 @@ __global__ void __launch_bounds__(Cfg<H, F8>::kThreads, 1)
       }
       if (!ok) break;
       // ---- epilogue: per-head sums across the 128 token rows, then O^T / l
-#pragma unroll
-      for (int hh = 0; hh < H; ++hh) {
-        float v = l_part[hh];
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        if (lane == (hh & 31)) red_s[q * H + hh] = v;
-      }
+      const float lw = over_lanes<H>(l_part, [](float u, float v) { return u + v; });
+      if (lane < H) red_s[q * H + lane] = lw;
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(bar + C::bLsum);
       if (!warp_wait(bar + C::bLsum, npc & 1, a.status, abort_flag)) { ok = false; break; }
-      float inv[H];
-#pragma unroll
-      for (int hh = 0; hh < H; ++hh) {
-        const float l = red_s[hh] + red_s[H + hh] + red_s[2 * H + hh] + red_s[3 * H + hh];
-        inv[hh] = l > 0.f ? 1.f / l : 0.f;
-        if (q == 0 && lane == 0)
-          lse_out[part_row(a.L, pc.piece, hh)] = l > 0.f ? (m_run[hh] + log2f(l)) * 0.69314718055994531f : -CUDART_INF_F;
-      }
+      const float l = red_s[hl] + red_s[H + hl] + red_s[2 * H + hl] + red_s[3 * H + hl];
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      if (q == 0 && lane < H)
+        lse_out[part_row(a.L, pc.piece, lane)] = l > 0.f ? (m_run + log2f(l)) * 0.69314718055994531f : -CUDART_INF_F;
       if (!warp_wait(bar + C::bODone + ((i - 1) & 1), ((i - 1) >> 1) & 1, a.status, abort_flag)) { ok = false; break; }
       ptx::tc_fence_after();
+      float *dst = opart + part_row(a.L, pc.piece, 0) * (long long)a.d_c + row;
+      const long long head_step = a.L.max_pieces * a.d_c;
 #pragma unroll 1
-      for (int f = 0; f < 4; ++f) {
+      for (int f = 0; f < 4; ++f, dst += 128) {
+        float *d = dst;
 #pragma unroll
         for (int c = 0; c < H / 16; ++c) {
           uint32_t r[16];
           ptx::tmem_ld16(lane_addr + C::kColO + f * H + 16 * c, r);
           ptx::tmem_ld_wait();
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const int hh = 16 * c + j;
-            opart[part_row(a.L, pc.piece, hh) * (long long)a.d_c + 128 * f + row] = __uint_as_float(r[j]) * inv[hh];
-          }
+          for (int j = 0; j < 16; ++j, d += head_step)
+            *d = __uint_as_float(r[j]) * __shfl_sync(0xffffffffu, inv, 16 * c + j);
         }
       }
       ptx::tc_fence_before();
