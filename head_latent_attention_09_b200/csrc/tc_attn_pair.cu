@@ -340,8 +340,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     // --------------------------------------------------------------- producer
     // Fills the ring in the order the MMAs consume it: the nine K chunks of
-    // tile i, then the V sub-stages of tile i-1 (tiles counted across the
-    // share's pieces).  A slot's full barrier (the leader's) takes an arrival
+    // tile i, then the V sub-stages of tile i-1; at the end of a piece its last
+    // tile's V comes before the next piece's K, which waits for another Q.  A slot's full barrier (the leader's) takes an arrival
     // from each CTA; the leader's also arms it with the bytes both CTAs' loads
     // bring (the peer's loads count on the leader's barrier directly).  One
     // elected thread does it all, in few instructions a slot (the MMAs want
@@ -395,11 +395,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (!kTree && tok0 + kSubTok > p.ctx) {
               // The block runs past the sequence: its load completes on a
               // barrier of its own, where the helper warp waits, which zeroes
-              // the rows past the end and then arrives for this CTA.  Such
-              // blocks follow one another at once only where a share's last
-              // two tiles both have one (no K chunks come between their V), so
-              // with two sets of barriers and slot numbers the set's previous
-              // block lies more than a ring back and has been consumed.
+              // the rows past the end and then arrives for this CTA.  Between
+              // two such blocks lie nine K chunks, more than a ring; with two
+              // sets of barriers and slot numbers nothing rests on that count.
               if (!ptx::mbar_wait(bars.empty(slot), phase, a.status, abort_flag)) return false;
               end_slot[2 * (nend & 1) + g] = slot;
               ptx::mbar_arrive_expect_tx(bars.end(nend, g), kSlot);
@@ -419,12 +417,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       int vt0 = 0, npc = 0;
       bool vpending = false, ok = true;
       while (ok && walk_next<kTree, kInl>(w, a, share, pc)) {
+        if (vpending && !issue_v(vpc, vt0, vx)) break;
+        vpending = false;
         if (npc > 0 && !ptx::mbar_wait(bars.qempty(), (npc - 1) & 1, a.status, abort_flag)) break;
         if (leader) ptx::mbar_arrive_expect_tx(bars.qfull(), 2 * kQBytes);
+#pragma unroll 1
         for (int c = 0; c < 9; ++c) {
           if (kTree)   // rows past the sequence's are zero-filled
-            ptx::tma_load_3d_pair(sQ + c * 8192, &mapQ, lq, 64 * c,
-                                  128 * pc.g + 64 * (int)rank, pc.b);
+            ptx::tma_load_3d_pair(sQ + c * 8192, &mapQ, lq, 64 * c, 128 * pc.g + 64 * (int)rank, pc.b);
           else
             ptx::tma_load_2d_pair(sQ + c * 8192, &mapQ, lq, 64 * c, pc.b * 128 + 64 * (int)rank);
         }
@@ -549,6 +549,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         return true;
       };
       while (ok && walk_next<kTree, kInl>(w, a, share, pc)) {
+        // The previous piece's last P.V goes first: this piece's S waits for its
+        // Q, which is loaded once the previous piece's last S is done (a
+        // piece's output is ready 2 to 3 us earlier than behind that S).
+        if (have_prev && !pv(prev)) { ok = false; break; }
+        have_prev = false;
         if (!ptx::mbar_wait(bars.qfull(), npc & 1, a.status, abort_flag)) { ok = false; break; }
         for (int k = 0; k < pc.ntiles && ok; ++k) {
           const uint32_t dS = tmem + (i & 1) * kColS;

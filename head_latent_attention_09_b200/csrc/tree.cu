@@ -11,6 +11,15 @@ template <typename T> __device__ __forceinline__ T cast(float x);
 template <> __device__ __forceinline__ float cast<float>(float x) { return x; }
 template <> __device__ __forceinline__ __nv_bfloat16 cast<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
 
+template <int V>
+struct alignas(4 * V) Vec {
+  float e[V];
+};
+template <typename T, int V>
+struct alignas(sizeof(T) * V) Out {
+  T e[V];
+};
+
 // Log-sum-exp merge of the groups that are split between shares.  A share
 // boundary cuts at most one plan sequence (gang groups), so block x takes
 // member x % gang of the one that begins in share x / gang and runs on into
@@ -19,8 +28,9 @@ template <> __device__ __forceinline__ __nv_bfloat16 cast<__nv_bfloat16>(float x
 // traffic is that of at most 2 P gang pieces however many groups there are.
 // The first two partials of a row (mostly all there are) are requested before
 // their log-sum-exps are used; one wave of blocks covers every share.
-template <typename T>
+template <typename T, int V>   // V columns to a lane and step: 4, or 1 where the widths or pointers forbid it
 __global__ void __launch_bounds__(256) tree_combine_kernel(AttnArgs a) {
+  constexpr int kSteps = 16 / V;   // d_c <= 512
   pdl_trigger();
   pdl_wait();
   const long long w0 = blockIdx.x / a.tree.gang;
@@ -55,13 +65,16 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(AttnArgs a) {
   // partials: the last piece of share w0 (or its only one), the first of the others
   auto part = [&](long long w) { return part_row(a.L, tree_piece(a, tp, v, w, member, P, Ttot).slot, r); };
   const long long pr0 = part(w0), pr1 = part(w0 + 1);
-  float v0[16], v1[16];
+  Vec<V> v0[kSteps], v1[kSteps];
+  const int f0 = lane * V;
+  auto request = [&](long long pr, Vec<V>(&v)[kSteps]) {
+    const float *src = op + pr * a.d_c + f0;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int f = lane + 32 * i;
-    v0[i] = f < a.d_c ? op[pr0 * a.d_c + f] : 0.f;
-    v1[i] = f < a.d_c ? op[pr1 * a.d_c + f] : 0.f;
-  }
+    for (int i = 0; i < kSteps; ++i)
+      if (f0 + 32 * V * i < a.d_c) v[i] = *reinterpret_cast<const Vec<V> *>(src + 32 * V * i);
+  };
+  request(pr0, v0);
+  request(pr1, v1);
   float m = -CUDART_INF_F;
   for (long long w = w0 + lane; w <= w1; w += 32) m = fmaxf(m, lse[part(w)]);
 #pragma unroll
@@ -77,17 +90,26 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(AttnArgs a) {
   const float wt0 = expf(lse[pr0] - m_use) * inv, wt1 = expf(lse[pr1] - m_use) * inv;
   const long long orow = (long long)b * a.tree.seq_rows + row;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) v0[i] = wt0 * v0[i] + wt1 * v1[i];
+  for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+    for (int e = 0; e < V; ++e) v0[i].e[e] = wt0 * v0[i].e[e] + wt1 * v1[i].e[e];
   for (long long w = w0 + 2; w <= w1; ++w) {
     const long long pr = part(w);
     const float wt = expf(lse[pr] - m_use) * inv;
+    request(pr, v1);
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (lane + 32 * i < a.d_c) v0[i] += wt * op[pr * a.d_c + lane + 32 * i];
+    for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+      for (int e = 0; e < V; ++e) v0[i].e[e] += wt * v1[i].e[e];
   }
 #pragma unroll
-  for (int i = 0; i < 16; ++i)
-    if (lane + 32 * i < a.d_c) out[orow * a.d_c + lane + 32 * i] = cast<T>(v0[i]);
+  for (int i = 0; i < kSteps; ++i) {
+    if (f0 + 32 * V * i >= a.d_c) continue;
+    Out<T, V> o;
+#pragma unroll
+    for (int e = 0; e < V; ++e) o.e[e] = cast<T>(v0[i].e[e]);
+    *reinterpret_cast<Out<T, V> *>(out + orow * a.d_c + f0 + 32 * V * i) = o;
+  }
   if (a.tree.lse && lane == 0) a.tree.lse[orow] = tot == 0.f ? -CUDART_INF_F : m_use + logf(tot);
 }
 
@@ -151,8 +173,10 @@ cudaError_t accept_units(int row_bytes, void *cache, const AttnArgs &a, const in
 cudaError_t launch_tree_combine(const AttnArgs &a, int P, bool fp32, cudaStream_t s) {
   const dim3 grid(P * a.tree.gang, (a.tree.group_rows + 7) / 8);
   if (grid.y > 65535 || a.d_c > 512) return cudaErrorNotSupported;
-  return fp32 ? launch_pdl(tree_combine_kernel<float>, grid, dim3(256), 0, s, 1, a)
-              : launch_pdl(tree_combine_kernel<__nv_bfloat16>, grid, dim3(256), 0, s, 1, a);
+  const bool wide = a.d_c % 4 == 0 && (uintptr_t)a.tree.out % 16 == 0;
+  auto go = [&](auto kern) { return launch_pdl(kern, grid, dim3(256), 0, s, 1, a); };
+  if (fp32) return wide ? go(tree_combine_kernel<float, 4>) : go(tree_combine_kernel<float, 1>);
+  return wide ? go(tree_combine_kernel<__nv_bfloat16, 4>) : go(tree_combine_kernel<__nv_bfloat16, 1>);
 }
 
 cudaError_t launch_tree_accept(const mla_config &cfg, void *cache, long long cache_len, const int *block_table,
