@@ -249,15 +249,18 @@ __global__ void __launch_bounds__(kSThreads, 1)
   const int q = warp & 3;
   const bool epi = warp >= 2;
   float acc[kSMaxTiles] = {0.f, 0.f, 0.f, 0.f};           // thread t of the epilogue: block t of each tile
-  // Columns [64 g, 64 g + 64) of this thread's row of tile t, in log2 units.
-  auto row64 = [&](int t, int g, float (&v)[64]) {
-    ptx::tmem_ld64_sync(tmem + ((uint32_t)(q * 32) << 16) + t * kScoreTile + 64 * g, reinterpret_cast<uint32_t *>(v));
-    const int jb = j0 + t * kScoreTile + 64 * g;
+  // Columns [32 g, 32 g + 32) of this thread's row over the CTA's tiles, in log2
+  // units.  (32 at a time: the passes run a few times each, so their code is
+  // fetched about as often as it runs, and its length counts.)
+  auto row32 = [&](int g, float (&v)[32]) {
+    ptx::tmem_ld32_sync(tmem + ((uint32_t)(q * 32) << 16) + 32 * g, reinterpret_cast<uint32_t *>(v));
+    const int jb = j0 + 32 * g;
     const float last = log2_tokens(nb - 1, ctx);
 #pragma unroll
-    for (int j = 0; j < 64; ++j)
+    for (int j = 0; j < 32; ++j)
       v[j] = jb + j < nb ? fmaf(v[j], scale_log2, jb + j == nb - 1 ? last : 6.f) : -CUDART_INF_F;
   };
+  const int groups = min((nb - j0 + 31) / 32, own * 4);   // 32-column groups that hold blocks
   for (int ht = 0; ht < head_tiles; ++ht) {
     if (warp == 0) {
       if (own > 0 && ptx::elect_one()) {
@@ -300,22 +303,21 @@ __global__ void __launch_bounds__(kSThreads, 1)
       __syncwarp();
       if (ok && ht * 128 + 32 * q < n_h) {
         ptx::tc_fence_after();
-        for (int t = 0; t < own; ++t)
 #pragma unroll 1
-          for (int g = 0; g < 2; ++g) {
-            float v[64];
-            row64(t, g, v);
-            float mx[4] = {m, m, m, m};
+        for (int g = 0; g < groups; ++g) {
+          float v[32];
+          row32(g, v);
+          float mx[4] = {m, m, m, m};
 #pragma unroll
-            for (int j = 0; j < 64; ++j) mx[j & 3] = fmaxf(mx[j & 3], v[j]);
-            const float m2 = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-            if (m2 == -CUDART_INF_F) continue;             // no block of the sequence among them
-            float s4[4] = {0.f, 0.f, 0.f, 0.f};
+          for (int j = 0; j < 32; ++j) mx[j & 3] = fmaxf(mx[j & 3], v[j]);
+          const float m2 = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          if (m2 == -CUDART_INF_F) continue;               // scores of -inf so far
+          float s4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int j = 0; j < 64; ++j) s4[j & 3] += ptx::exp2_approx(v[j] - m2);
-            sum = sum * exp2f(m - m2) + ((s4[0] + s4[1]) + (s4[2] + s4[3]));
-            m = m2;
-          }
+          for (int j = 0; j < 32; ++j) s4[j & 3] += ptx::exp2_approx(v[j] - m2);
+          sum = sum * exp2f(m - m2) + ((s4[0] + s4[1]) + (s4[2] + s4[3]));
+          m = m2;
+        }
       }
       stat[ht & 1][32 * q + lane] = h < n_h ? make_float2(m, sum) : make_float2(-CUDART_INF_F, 0.f);
     }
@@ -337,30 +339,25 @@ __global__ void __launch_bounds__(kSThreads, 1)
         }
         const bool real = ht * 128 + h < n_h;
         const float lse = real ? m + log2f(sum) : 0.f;
-        for (int t = 0; t < own; ++t)
 #pragma unroll 1
-          for (int g = 0; g < 2; ++g) {
-            float v[64];
-            row64(t, g, v);
+        for (int g = 0; g < groups; ++g) {
+          float v[32];
+          row32(g, v);
 #pragma unroll
-            for (int j = 0; j < 64; ++j) v[j] = real ? ptx::exp2_approx(v[j] - lse) : 0.f;
-            // Sums over the 32 lanes: halving the columns a lane is in charge
-            // of with every exchange leaves lane l columns l and 32 + l.
+          for (int j = 0; j < 32; ++j) v[j] = real ? ptx::exp2_approx(v[j] - lse) : 0.f;
+          // Sums over the 32 lanes: halving the columns a lane is in charge of
+          // with every exchange leaves lane l column l.
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-              const bool up = (lane & o) != 0;
+          for (int o = 16; o > 0; o >>= 1) {
+            const bool up = (lane & o) != 0;
 #pragma unroll
-              for (int hlf = 0; hlf < 2; ++hlf)
-#pragma unroll
-                for (int j = 0; j < o; ++j) {
-                  float *w = v + 32 * hlf;
-                  const float give = up ? w[j] : w[j + o], keep = up ? w[j + o] : w[j];
-                  w[j] = keep + __shfl_xor_sync(0xffffffffu, give, o);
-                }
+            for (int j = 0; j < o; ++j) {
+              const float give = up ? v[j] : v[j + o], keep = up ? v[j + o] : v[j];
+              v[j] = keep + __shfl_xor_sync(0xffffffffu, give, o);
             }
-            part[q][t * kScoreTile + 64 * g + lane] = v[0];
-            part[q][t * kScoreTile + 64 * g + 32 + lane] = v[32];
           }
+          part[q][32 * g + lane] = v[0];
+        }
       }
       ptx::named_bar_sync(1, 128);
       const int warps = min(4, (n_h - ht * 128 + 31) / 32);    // epilogue warps that hold heads
