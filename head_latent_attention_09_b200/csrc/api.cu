@@ -56,6 +56,12 @@ int default_parts(const mla_handle *h) {
   }
 }
 
+// The handle's device is the current one (its status word and tables live there).
+bool on_device(const mla_handle *h) {
+  int dev = -1;
+  return cudaGetDevice(&dev) == cudaSuccess && dev == h->device;
+}
+
 bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
 
 // Tokens per tile of the split plan: the MMA tile of the attention kernel the
@@ -233,7 +239,7 @@ int mla_cache_append_tree(mla_handle *h, const void *x, int B, int T, const int 
                           const void *w_dkv, const void *w_kr, void *cache, long long cache_len,
                           const int *block_table, int max_blocks_per_seq, mla_stream_t stream) {
   Range range("mla_cache_append_tree");
-  if (!h || T > kTreeMaxDrafted || (!depth && B > 0 && T > 0)) return MLA_ERR_INVALID_ARG;
+  if (!h || T > kTreeMaxDrafted || (B > 0 && T > 0 && (!depth || !on_device(h)))) return MLA_ERR_INVALID_ARG;
   return cache_append(h, x, B, T, ctx_len, depth, w_dkv, w_kr, cache, cache_len, block_table, max_blocks_per_seq,
                       stream);
 }
@@ -320,9 +326,9 @@ int decode_attn(mla_handle *h, const void *q_abs, const void *cache, const float
   a.cap = cap;
   // The tensor-core kernels plan for themselves, up to kInlineSeqs sequences
   // (the one for 32 heads over an FP8 cache has no shared memory left for it).
-  const Before plan = [&] { return launch_plan(src, B, P, cap, tile, (char *)workspace, L, h->d_status, s); };
+  const auto plan = [&] { return launch_plan(src, B, P, cap, tile, (char *)workspace, L, h->d_status, s); };
   a.inline_plan = B <= kInlineSeqs && !(kv_scale && c.n_h > 16);
-  const Before before = a.inline_plan ? Before() : plan;
+  const Before before = a.inline_plan ? Before() : Before(plan);
   cudaError_t e = cudaErrorNotSupported;
   if (h->attn_kind == kAttnTcPair && !kv_scale && aligned16(q_abs) && aligned16(cache))
     e = launch_attn_tc_pair(a, P, s, before);
@@ -372,7 +378,7 @@ int mla_decode_attn_sparse(mla_handle *h, const void *q_abs, const void *cache, 
                            mla_stream_t stream) {
   Range range("mla_decode_attn_sparse");
   if (!h || k < 0 || k > kMaxSelected) return MLA_ERR_INVALID_ARG;
-  if (B > 0 && (k == 0 || !sel || !n_sel)) return MLA_ERR_INVALID_ARG;
+  if (B > 0 && (k == 0 || !sel || !n_sel || !on_device(h))) return MLA_ERR_INVALID_ARG;
   if (h->cfg.page_size % kTile != 0) return MLA_ERR_UNSUPPORTED;   // a block's rows must be consecutive
   PlanSource src{ctx_len};
   src.sel = sel;
@@ -455,7 +461,7 @@ int mla_tree_attn(mla_handle *h, const void *q_abs, const void *cache, long long
   if (B == 0 || T == 0) return MLA_OK;
   if (!q_abs || !cache || !ctx_len || !tree_mask || !ctx_lat) return MLA_ERR_INVALID_ARG;
   const mla_config &c = h->cfg;
-  if (!table_ok(c, block_table, max_blocks_per_seq)) return MLA_ERR_INVALID_ARG;
+  if (!table_ok(c, block_table, max_blocks_per_seq) || !on_device(h)) return MLA_ERR_INVALID_ARG;
   size_t need = 0;
   const int st = mla_tree_workspace_size(h, B, T, num_parts, &need);
   if (st != MLA_OK) return st;
@@ -497,7 +503,8 @@ int mla_tree_attn(mla_handle *h, const void *q_abs, const void *cache, long long
     if (tc) {
       // the tensor maps are made before anything is launched
       if (!aligned16(q_abs) || !aligned16(cache) || !aligned16(ctx_lat)) return cudaErrorNotSupported;
-      e = launch_tree_attn_tc_pair(a, t.parts, s, [&] { return launch_tree_plan_copy(src, a, t.parts, cap, s); });
+      const auto plan = [&] { return launch_tree_plan_copy(src, a, t.parts, cap, s); };
+      e = launch_tree_attn_tc_pair(a, t.parts, s, Before(plan));
     } else {
       e = launch_plan(src, a.B, t.parts, cap, t.tile, a.ws, a.L, a.status, s);
       if (e == cudaSuccess) e = launch_tree_attn_simt(a, t.parts, c.dtype == MLA_FP32, s);
@@ -519,7 +526,7 @@ int mla_tree_accept(mla_handle *h, void *cache, long long cache_len, const int *
   if (!h || B < 0 || T < 0 || T > kTreeMaxDrafted || cache_len < 0) return MLA_ERR_INVALID_ARG;
   if (B == 0 || T == 0) return MLA_OK;
   if (!cache || !ctx_len || !path || !n_path) return MLA_ERR_INVALID_ARG;
-  if (!table_ok(h->cfg, block_table, max_blocks_per_seq)) return MLA_ERR_INVALID_ARG;
+  if (!table_ok(h->cfg, block_table, max_blocks_per_seq) || !on_device(h)) return MLA_ERR_INVALID_ARG;
   const cudaError_t e = launch_tree_accept(h->cfg, cache, cache_len, block_table, max_blocks_per_seq, ctx_len, path,
                                            n_path, B, T, new_len, h->d_status, (cudaStream_t)stream);
   return e == cudaErrorNotSupported ? MLA_ERR_UNSUPPORTED : from_cuda(e);
@@ -532,7 +539,7 @@ int mla_block_keys(mla_handle *h, const void *cache, long long cache_len, const 
   if (!h || B < 0 || max_new < 0 || key_blocks < 0 || cache_len < 0) return MLA_ERR_INVALID_ARG;
   if (B == 0 || max_new == 0) return MLA_OK;
   if (!cache || !ctx_len || !keys || key_blocks == 0) return MLA_ERR_INVALID_ARG;
-  if (!table_ok(h->cfg, block_table, max_blocks_per_seq)) return MLA_ERR_INVALID_ARG;
+  if (!table_ok(h->cfg, block_table, max_blocks_per_seq) || !on_device(h)) return MLA_ERR_INVALID_ARG;
   const cudaError_t e = launch_block_keys(h->cfg, cache, cache_len, block_table, max_blocks_per_seq, ctx_begin,
                                           ctx_len, B, max_new, keys, key_blocks, h->d_status, (cudaStream_t)stream);
   return e == cudaErrorNotSupported ? MLA_ERR_UNSUPPORTED : from_cuda(e);
@@ -549,7 +556,7 @@ int mla_block_scores(mla_handle *h, const void *q_abs, const void *keys, int key
   Range range("mla_block_scores");
   if (!h || B < 0 || key_blocks < 0) return MLA_ERR_INVALID_ARG;
   if (B == 0 || key_blocks == 0) return MLA_OK;
-  if (!q_abs || !keys || !ctx_len || !scores) return MLA_ERR_INVALID_ARG;
+  if (!q_abs || !keys || !ctx_len || !scores || !on_device(h)) return MLA_ERR_INVALID_ARG;
   const ScoreLayout L = score_layout(h->cfg, B, key_blocks);
   if (!workspace || ((uintptr_t)workspace & 255u) || ws_bytes < L.total) return MLA_ERR_WORKSPACE;
   const bool tc = h->cfg.dtype == MLA_BF16 && h->cfg.d_c == 512 && h->cfg.d_r == 64;
@@ -570,7 +577,8 @@ int mla_block_select(mla_handle *h, const float *scores, int key_blocks, const i
   if (!h || B < 0 || key_blocks < 0 || k < 0 || k > kMaxSelected || n_first < 0 || n_last < 0)
     return MLA_ERR_INVALID_ARG;
   if (B == 0) return MLA_OK;
-  if (!ctx_len || !n_sel || (key_blocks > 0 && !scores) || (k > 0 && !sel)) return MLA_ERR_INVALID_ARG;
+  if (!ctx_len || !n_sel || (key_blocks > 0 && !scores) || (k > 0 && !sel) || !on_device(h))
+    return MLA_ERR_INVALID_ARG;
   const cudaError_t e = launch_block_select(scores, key_blocks, ctx_len, B, k, n_first, n_last, sel, n_sel,
                                             h->d_status, (cudaStream_t)stream);
   return e == cudaErrorNotSupported ? MLA_ERR_UNSUPPORTED : from_cuda(e);

@@ -8,7 +8,6 @@
 
 #include <algorithm>
 #include <atomic>
-#include <functional>
 #include <mutex>
 
 #include "mla.h"
@@ -445,7 +444,19 @@ cudaError_t launch_combine_outproj_tc(const mla_config &cfg, const char *ws, con
                                       cudaStream_t s);
 // `before` launches what goes before the kernel (a plan, a copy), once the
 // arguments are known to be ones it can take.
-using Before = std::function<cudaError_t()>;
+class Before {   // refers to a callable that outlives it (or to none); owns nothing and never throws
+ public:
+  Before() = default;
+  template <typename Fn>
+  explicit Before(const Fn &fn)
+      : what_(&fn), call_([](const void *w) { return (*static_cast<const Fn *>(w))(); }) {}
+  explicit operator bool() const { return call_ != nullptr; }
+  cudaError_t operator()() const { return call_(what_); }
+
+ private:
+  const void *what_ = nullptr;
+  cudaError_t (*call_)(const void *) = nullptr;
+};
 cudaError_t launch_attn_tc_pair(const AttnArgs &a, int P, cudaStream_t s, const Before &before);
 // The same kernel over a tree of drafted tokens, 128 query rows at a time.
 cudaError_t launch_tree_attn_tc_pair(const AttnArgs &a, int P, cudaStream_t s, const Before &before);

@@ -430,12 +430,15 @@ int mla_decode_attn_fp8(mla_handle *handle, const void *q_abs, const void *cache
  *   mla_out_proj            with B * T rows
  * and, once the accepted branch is known,
  *   mla_tree_accept         its rows move together behind the sequence.
+ * These calls, and those of the block selection below, want the handle's device
+ * to be the current one (MLA_ERR_INVALID_ARG otherwise).
  * ------------------------------------------------------------------------- */
 
 /* mla_cache_append with separate slots and rotary positions: token t of
  * sequence b is written at position ctx_len[b] + t and rotated by
  * ctx_len[b] + depth[b, t].
- *   depth  device int32 [B, T]
+ *   depth  device int32 [B, T] (its values are not checked: they only turn the
+ *          rotary part)
  * T at most 64; other arguments and errors as for mla_cache_append. */
 int mla_cache_append_tree(mla_handle *handle, const void *h, int B, int T, const int *ctx_len, const int *depth,
                           const void *w_dkv, const void *w_kr, void *cache, long long cache_len,
@@ -529,7 +532,9 @@ int mla_block_scores_workspace_size(const mla_handle *handle, int B, int key_blo
  *   q_abs [B, n_h, d_c+d_r], keys [B, key_blocks, d_c+d_r], scores float32 [B, key_blocks]
  * A sequence with more than key_blocks blocks is scored over the first
  * key_blocks and flagged MLA_ERR_DEVICE_BOUNDS.  bf16 rows of d_c = 512, d_r = 64
- * run on the tensor cores.  Errors: INVALID_ARG, WORKSPACE, UNSUPPORTED, CUDA. */
+ * with up to 4096 blocks (262144 tokens) run on the tensor cores, others on the
+ * CUDA cores (not in strict mode).  Errors: INVALID_ARG, WORKSPACE, UNSUPPORTED
+ * (B above 65535, n_h above 12288), CUDA. */
 int mla_block_scores(mla_handle *handle, const void *q_abs, const void *keys, int key_blocks, const int *ctx_len,
                      int B, float *scores, void *workspace, size_t ws_bytes, mla_stream_t stream);
 
