@@ -316,3 +316,71 @@ def test_wrong_blocks_are_flagged_and_not_read(sh):
                                  2, 0, ws, size)
         assert M.mla_get_device_status(h) == M.MLA_ERR_DEVICE_BOUNDS, (sel, n)
     M.mla_destroy(h)
+
+
+@pytest.mark.parametrize("sh,page", [(shape(LITE), 64), (shape(V2), 0), (shape(TINY), 16)])
+def test_guard_bands_streams_and_graphs(sh, page):
+    """Nothing is written outside the outputs; the calls are the same on another
+    stream, and captured and replayed on other inputs."""
+    rng = np.random.default_rng(3)
+    D, B, k, blocks = sh["d_c"] + sh["d_r"], 3, 4, 12
+    ctx, ctx2 = [700, 63, 321], [128, 700, 1]
+    h = handle(sh, page)
+    caches = [Cache(sh, [stored(sh, rng.standard_normal((n, D))) for n in c], 700, page, np.random.default_rng(1))
+              for c in (ctx, ctx2)]
+    dt, raws = torch_type(sh), []
+
+    def buffer(shape_, dtype):
+        n = int(np.prod(shape_)) * torch.empty((), dtype=dtype).element_size()
+        raws.append(torch.full((n + 8192,), 0x5A, dtype=torch.uint8, device="cuda"))
+        return raws[-1][4096:-4096].view(dtype).view(shape_)
+
+    keys, scores = buffer((B, blocks, D), dt), buffer((B, blocks), torch.float32)
+    sel, n_sel = buffer((B, k), torch.int32), buffer((B,), torch.int32)
+    sws = buffer((M.mla_block_scores_workspace_size(h, B, blocks),), torch.uint8)
+    sparse = page % 64 == 0
+    ws = buffer((M.mla_decode_workspace_size(h, B, 0),), torch.uint8)
+    out = buffer((B, sh["n_h"], sh["d_c"]), dt)
+    q = dev(sh, rng.standard_normal((B, sh["n_h"], D)) * 0.7)
+    data, lens = caches[0].data.clone(), ints(ctx)
+    args = (data, caches[0].len, caches[0].table, caches[0].max_blk)
+
+    def call(st):
+        M.mla_block_keys(h, *args, None, lens, B, 700, keys, blocks, st)
+        M.mla_block_scores(h, q, keys, blocks, lens, B, scores, sws, sws.numel(), st)
+        M.mla_block_select(h, scores, blocks, lens, B, k, 1, 1, sel, n_sel, st)
+        if sparse:
+            M.mla_decode_attn_sparse(h, q, *args, lens, sel, n_sel, k, B, 0, ws, ws.numel(), st)
+            M.mla_combine_splits(h, ws, ws.numel(), B, 0, out, None, st)
+
+    def results():
+        torch.cuda.synchronize()
+        valid = [-(-n // 64) for n in lens.tolist()]
+        return [host(keys)[b, :v] for b, v in enumerate(valid)] + [host(x) for x in (scores, sel, n_sel, *((out,) if sparse else ()))]
+
+    want = []
+    for c, cache in ((ctx, caches[0]), (ctx2, caches[1])):
+        data.copy_(cache.data)
+        lens.copy_(ints(c))
+        call(None)
+        want.append(results())
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        call(torch.cuda.current_stream())
+    data.copy_(caches[0].data)
+    lens.copy_(ints(ctx))
+    torch.cuda.synchronize()
+    call(s)
+    assert all(np.array_equal(a, b) for a, b in zip(results(), want[0]))
+    data.copy_(caches[1].data)
+    lens.copy_(ints(ctx2))
+    for _ in range(2):
+        out.fill_(0)
+        g.replay()
+    assert all(np.array_equal(a, b) for a, b in zip(results(), want[1]))
+    ok(h)
+    for r in raws:
+        assert (r[:4096] == 0x5A).all() and (r[-4096:] == 0x5A).all()
+    M.mla_destroy(h)
