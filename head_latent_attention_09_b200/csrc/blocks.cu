@@ -153,6 +153,11 @@ __device__ __forceinline__ float log2_tokens(int j, int ctx) {
   return n >= kTile ? 6.f : log2f((float)n);
 }
 
+// Maxima are subtracted through this: scores of -inf alone (overflows) then add
+// nothing (-inf - -inf is NaN), while a NaN, which no maximum shows, still
+// reaches the sum and with it every share of the head.
+__device__ __forceinline__ float minus_inf_to_0(float m) { return m == -CUDART_INF_F ? 0.f : m; }
+
 // CUDA cores, two launches: first x and the statistics, one warp per head, the
 // query row in registers (also bf16 beyond the tensor-core kernel's 4096 blocks).
 template <typename T>
@@ -184,8 +189,8 @@ __global__ void __launch_bounds__(256) score_logits_simt_kernel(const T *q_abs, 
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
     x = x * scale_log2 + log2_tokens(j, ctx);
-    const float m2 = fmaxf(m, x);
-    sum = sum * exp2f(m - m2) + exp2f(x - m2);
+    const float m2 = fmaxf(m, x), m_use = minus_inf_to_0(m2);
+    sum = sum * exp2f(m - m_use) + exp2f(x - m_use);
     m = m2;
     if (lane == 0) logits[((long long)b * L.tiles * kScoreTile + j) * L.head_rows + h] = x;
   }
@@ -311,11 +316,11 @@ __global__ void __launch_bounds__(kSThreads, 1)
 #pragma unroll
           for (int j = 0; j < 32; ++j) mx[j & 3] = fmaxf(mx[j & 3], v[j]);
           const float m2 = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-          if (m2 == -CUDART_INF_F) continue;               // scores of -inf so far
+          const float m_use = minus_inf_to_0(m2);
           float s4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int j = 0; j < 32; ++j) s4[j & 3] += ptx::exp2_approx(v[j] - m2);
-          sum = sum * exp2f(m - m2) + ((s4[0] + s4[1]) + (s4[2] + s4[3]));
+          for (int j = 0; j < 32; ++j) s4[j & 3] += ptx::exp2_approx(v[j] - m_use);
+          sum = sum * exp2f(m - m_use) + ((s4[0] + s4[1]) + (s4[2] + s4[3]));
           m = m2;
         }
       }
@@ -332,9 +337,8 @@ __global__ void __launch_bounds__(kSThreads, 1)
         const int nc = (int)ptx::cluster_nctarank();
         for (int p = 0; p < nc; ++p) {
           const float2 s = ptx::ld_shared_cluster_v2f(ptx::mapa_peer(mine, (uint32_t)p));
-          if (s.x == -CUDART_INF_F) continue;
-          const float m2 = fmaxf(m, s.x);
-          sum = sum * exp2f(m - m2) + s.y * exp2f(s.x - m2);
+          const float m2 = fmaxf(m, s.x), m_use = minus_inf_to_0(m2);
+          sum = sum * exp2f(m - m_use) + s.y * exp2f(s.x - m_use);
           m = m2;
         }
         const bool real = ht * 128 + h < n_h;
@@ -400,7 +404,7 @@ __global__ void __launch_bounds__(256) score_sum_kernel(const float *logits, con
       for (int t = 0; t < tiles; ++t) m = fmaxf(m, st[(long long)t * L.head_rows].x);
       for (int t = 0; t < tiles; ++t) {
         const float2 v = st[(long long)t * L.head_rows];
-        sum += v.y * exp2f(v.x - m);
+        sum += v.y * exp2f(v.x - minus_inf_to_0(m));
       }
       lse[h] = m + log2f(sum);
     }

@@ -384,3 +384,33 @@ def test_guard_bands_streams_and_graphs(sh, page):
     for r in raws:
         assert (r[:4096] == 0x5A).all() and (r[-4096:] == 0x5A).all()
     M.mla_destroy(h)
+
+
+@pytest.mark.parametrize("at", [[0], list(range(32)), list(range(32, 64)), list(range(128)), list(range(128, 256)), [299]])
+@pytest.mark.parametrize("sh", [shape(LITE), shape(V2), shape(TINY)])
+def test_block_scores_of_nan_and_of_minus_infinity(sh, at):
+    """A mean row with a NaN makes every share of the sequence NaN, wherever it
+    stands; a block whose scores overflow to -inf draws nothing and changes no
+    other block."""
+    rng = np.random.default_rng(at[0])
+    blocks, D = 300, sh["d_c"] + sh["d_r"]
+    ctx = [64 * blocks, 64 * blocks - 9]
+    keys = stored(sh, rng.standard_normal((2, blocks, D)))
+    q = stored(sh, rng.standard_normal((2, sh["n_h"], D)) * 0.7)
+    h = handle(sh)
+    bad = keys.copy()
+    bad[0, at, 5] = np.nan
+    got = scores_of(sh, h, q, bad, ctx, blocks)
+    assert np.isnan(got[0]).all()
+    compare_scores(sh, got[1:], q[1:], keys[1:], ctx[1:])
+    keys[:, :, 0] = 0
+    q[:, :, 0] = stored(sh, np.array([1e20]))
+    bad = keys.copy()
+    bad[0, at, 0] = stored(sh, np.array([-1e20]))      # q . key = -1e40
+    got = scores_of(sh, h, q, bad, ctx, blocks)
+    ok(h)
+    M.mla_destroy(h)
+    rest = [j for j in range(blocks) if j not in at]
+    assert (got[0, at] == 0).all()
+    compare_scores(sh, got[:1, rest], q[:1], keys[:1, rest], [64 * len(rest)])
+    compare_scores(sh, got[1:], q[1:], keys[1:], ctx[1:])
