@@ -284,8 +284,10 @@ __global__ void __launch_bounds__(256) attn_simt_kernel(AttnArgs a) {
       for (int j = 0; j < kQPerLane; ++j) part += q[j] * val[j];
       const float s = warp_sum(part) * a.scale_log2;   // score in log2 units
       const float m_new = fmaxf(m, s);
-      const float corr = exp2f(m - m_new);
-      const float pr = exp2f(s - m_new);
+      // a tree's row whose scores have all overflowed to -inf so far: -inf - -inf is NaN
+      const float m_use = kTree && m_new == -CUDART_INF_F ? 0.f : m_new;
+      const float corr = exp2f(m - m_use);
+      const float pr = exp2f(s - m_use);
       l = l * corr + pr;
 #pragma unroll
       for (int j = 0; j < kOPerLane; ++j) {

@@ -396,3 +396,31 @@ def test_accept_leaves_a_sequence_with_a_wrong_path():
     M.mla_tree_accept(h, *cache.args, ints([12] * 7), ints([[0, 2, 0, 0]] * 7), ints([2] * 7), 7, T, new)
     assert M.mla_get_device_status(h) == M.MLA_ERR_DEVICE_BOUNDS and new.tolist() == [12] * 7
     M.mla_destroy(h)
+
+
+@pytest.mark.parametrize("ctx", [(0, 70), (300, 64)])
+@pytest.mark.parametrize("sh", [shape(LITE), shape(TINY)])
+def test_scores_that_overflow_to_minus_infinity(sh, ctx):
+    """A token whose score overflows to -inf draws nothing, the first one too."""
+    t = Tree(sh, ctx, 4, 9)
+    t.q[..., -1] = stored(sh, np.array([1e20]))
+    for r in t.rows:
+        r[:, -1] = 0
+    given = [r.copy() for r in t.rows]
+    for r in given:
+        r[0, -1] = stored(sh, np.array([-1e20]))       # q . row = -1e40
+    got = t.run(rows=given)
+    scale = O.softmax_scale(sh["d_h"], sh["d_r"])
+    for b, n in enumerate(ctx):
+        r = t.rows[b].astype(np.float64)
+        for k in range(t.T):
+            mine = np.concatenate([r[:n], r[n:][[j for j in range(t.T) if t.bits[b][k] >> j & 1]]])
+            mine = mine[1:] if n or t.bits[b][k] & 1 else mine
+            q = t.q[b, k].astype(np.float64)
+            if len(mine) == 0:
+                assert (got[0][b, k] == 0).all() and np.isneginf(got[1][b, k]).all()
+                continue
+            want, lse = O.latent_attention(q, mine, d_c=sh["d_c"], scale=scale)
+            bo, bl = attention_bounds(sh, q, mine, scale, want, lse)
+            within(got[0][b, k], want, bo, f"ctx_lat of sequence {b}, token {k}")
+            within(got[1][b, k], lse, bl, f"lse of sequence {b}, token {k}")
