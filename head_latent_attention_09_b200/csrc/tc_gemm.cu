@@ -94,6 +94,7 @@ struct GemmParams {
   int num_k_chunks;   // K / 64 of the whole product
   int stages;         // K-chunk slots of the ring (<= kMaxStages, a multiple of group)
   int group;          // K chunks per TMA load group (1, 2 or 4)
+  int per;            // K chunks of a slice (the last ones may have fewer, or none)
   int ksplit;         // K slices per output tile (1, or a cluster of ksplit CTAs along x)
   int mt_per_cta;     // 128-row m tiles one CTA computes, sharing its B tiles (1 when ksplit > 1)
   int m_tiles;        // m tiles of the whole product
@@ -170,7 +171,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   const int mt = ((int)blockIdx.x / g.ksplit) * MT, zs = (int)blockIdx.x % g.ksplit;
   const int mcount = min(MT, g.m_tiles - mt);
   const int nt = blockIdx.y, z = blockIdx.z;
-  const int per = (g.num_k_chunks + g.ksplit - 1) / g.ksplit;
+  const int per = g.per;
   const int kc0 = zs * per;
   const int nk = max(0, min(g.num_k_chunks, kc0 + per) - kc0);   // K chunks of this CTA
   const int ngrp = (nk + G - 1) / G;                               // load groups of this CTA
@@ -456,12 +457,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     ptx::cluster_sync_all();   // partials of all K slices are written
     const int ks = g.ksplit;
     if (ptx::cluster_nctarank() == (uint32_t)ks) {
-      // This CTA sums rows [zs*R, zs*R + R) of the tile over the cluster's
+      // This CTA sums its share of the tile's columns over the cluster's
       // partials, 4 rows (one float4) per item, and writes them out.
-      const int R = 128 / ks, R4 = R / 4;
       const uint32_t red = ptx::smem_u32(base);
-      for (int idx = threadIdx.x; idx < BN * R4; idx += kGemmThreads) {
-        const int c = idx / R4, ml = zs * R + 4 * (idx % R4);
+      const int i1 = (zs + 1) * (BN * 32) / ks;
+      for (int idx = zs * (BN * 32) / ks + threadIdx.x; idx < i1; idx += kGemmThreads) {
+        const int c = idx / 32, ml = 4 * (idx % 32);
         const uint32_t off = (uint32_t)((c * 128 + ml) * 4);
         // every peer's float4 in flight at once, summed in cluster-rank order
         float4 pv[8];
@@ -556,7 +557,7 @@ cudaError_t launch_gemm(const CUtensorMap &a0, const CUtensorMap &a1, const CUte
     return cudaErrorNotSupported;
   g.m_tiles = mtiles;
   const int chunk = g.mt_per_cta * kABytes + b_bytes<BN>();   // one K chunk's A and B
-  const int per = (g.num_k_chunks + g.ksplit - 1) / g.ksplit;
+  const int per = g.per;
   int max_chunks = (int)((kSmemLimit - 1024 - smem_tail<BN>()) / chunk);
   if (max_chunks > kMaxStages) max_chunks = kMaxStages;
   const int G = g.group;
@@ -580,17 +581,65 @@ cudaError_t launch_gemm(const CUtensorMap &a0, const CUtensorMap &a1, const CUte
   return launch_pdl(kern, grid, dim3(kGemmThreads), smem, s, g.ksplit, a0, a1, b, g);
 }
 
-// K split: the smallest power of two (<= 8, the portable cluster size) that
-// gives at least one CTA per SM, while every slice keeps >= 2 K chunks.  Tiles
-// of 256 columns take an SM's shared memory each, so there the split stops
-// before a second wave (1024 tokens of d = 5120: 20 CTAs x 8 in two waves 28
-// us, x 4 in one 20 us).
-int pick_ksplit(long long ctas, int num_k_chunks, int bn) {
+int sm_count() {
   int sms = 148, dev = 0;
   if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  int ks = 1;
-  while (ks < 8 && ctas * ks < sms && num_k_chunks >= 4 * ks && (bn < 256 || 2 * ctas * ks <= sms)) ks *= 2;
-  return ks;
+  return sms;
+}
+
+// Whether `tiles` clusters of ks CTAs that take an SM each run at once.
+// Clusters lie within GPCs: of 148 SMs 15 clusters of eight CTAs fit, 22 of six,
+// 26 of five, 33 of four, 45 of three.
+bool one_wave(long long tiles, int ks, int sms) {
+  if (ks <= 2) return tiles * ks <= sms;
+  return ks == 8 ? 10 * tiles <= sms : 8 * tiles * ks <= 7 * sms;
+}
+
+// K split: the smallest power of two (<= 8, the portable cluster size) that
+// gives at least one CTA per SM, while every slice keeps >= 2 K chunks.  Tiles
+// of 256 columns take an SM's shared memory each, so there it is the largest
+// split that stays in one wave.
+int pick_ksplit(long long ctas, int num_k_chunks, int bn) {
+  const int sms = sm_count();
+  if (bn < 256) {
+    int ks = 1;
+    while (ks < 8 && ctas * ks < sms && num_k_chunks >= 4 * ks) ks *= 2;
+    return ks;
+  }
+  for (int ks : {8, 6, 5, 4, 3, 2})
+    if (num_k_chunks >= 2 * ks && one_wave(ctas, ks, sms)) return ks;
+  return 1;
+}
+
+// K chunks of one slice.  Below 256 columns an even number where there are
+// several, so that a load group can hold two (128 columns: 27 chunks loaded one
+// by one took as long as 40 in pairs).
+int slice_chunks(int num_k_chunks, int ksplit, int bn) {
+  const int per = (num_k_chunks + ksplit - 1) / ksplit;
+  return ksplit > 1 && per > 1 && bn < 256 ? (per + 1) / 2 * 2 : per;
+}
+
+// Column tile and K split of the append, a product of few m tiles and a long K
+// (d of 2048 or 5120) whose time goes into streaming each CTA's operands (about
+// 94 KB a microsecond) and into the epilogue, which passes the tile's partials
+// through the cluster (24 ns a column): of the choices that run in one wave, the
+// one with the least of both.  At d = 5120 (us, and what a tile as wide as the
+// tokens allow took): 64 tokens 32 columns x 8 6.9 (7.4), 256 tokens 64 x 6 9.1
+// (13.8), 512 tokens 128 x 6 11.1 (14.5), 768 tokens 128 x 4 13.1 (16.6).
+void pick_append(int mtiles, long long N, int num_k_chunks, int *bn, int *ksplit) {
+  const int sms = sm_count();
+  double least = 1e30;
+  for (int n = N <= 16 ? 16 : 32; n <= 256 && n < 2 * std::max(N, 16ll); n *= 2)
+    for (int ks : {1, 2, 3, 4, 5, 6, 8}) {
+      const long long tiles = mtiles * ((N + n - 1) / n);
+      if (num_k_chunks < 2 * ks || !one_wave(tiles, ks, sms)) continue;
+      const double cost = slice_chunks(num_k_chunks, ks, n) * (16 + n / 8) / 94.0 + 0.024 * n;
+      if (cost < least) {
+        least = cost;
+        *bn = n;
+        *ksplit = ks;
+      }
+    }
 }
 
 int pick_bn(long long N) {
@@ -611,13 +660,17 @@ struct Maps {
 // tensor maps, and launches.
 template <bool A_MN, typename Encode>
 cudaError_t dispatch(int N, GemmParams g, int mtiles, int z, cudaStream_t s, Encode encode) {
-  const int bn = pick_bn(N);
+  int bn = pick_bn(N);
+  if (g.mode == kEpiAppend) pick_append(mtiles, N, g.num_k_chunks, &bn, &g.ksplit);
   const int ntiles = (N + bn - 1) / bn;
   if (g.mt_per_cta == 0) g.mt_per_cta = 1;
   if (g.ksplit == 0)
     g.ksplit = g.mt_per_cta > 1 ? 1 : pick_ksplit((long long)mtiles * ntiles * z, g.num_k_chunks, bn);
-  const int per = (g.num_k_chunks + g.ksplit - 1) / g.ksplit;
-  g.group = pick_group(per, bn, g.mt_per_cta);
+  g.per = slice_chunks(g.num_k_chunks, g.ksplit, bn);
+  const int per = g.per;
+  // A long slice of 256 columns keeps its four chunks in flight one by one (two
+  // pairs, refilled in turn: 2048 tokens of d = 5120 28.0 us, one by one 26.1).
+  g.group = bn == 256 && per > 4 ? 1 : pick_group(per, bn, g.mt_per_cta);
   Maps m;
   if (!encode(g.group, bn, m)) return cudaErrorNotSupported;
   switch (bn) {
