@@ -27,7 +27,9 @@ template <> __device__ __forceinline__ __nv_bfloat16 narrow<__nv_bfloat16>(float
 // column unit u (V elements, 16 bytes where the alignment allows) of the rows
 // g, g + G, ..., all loads of a batch in flight, and the G partial sums meet
 // in shared memory.  It reads every row once and writes 1/64 of that: bound
-// by HBM for a whole prompt, by the launch for a decode step.
+// by HBM for a whole prompt (four of 131072 tokens: 91 us, 6.66 TB/s of rows),
+// by the launch and three dependent reads for a decode step (one block of each
+// of 64 sequences: 6.8 us).
 // ---------------------------------------------------------------------------
 constexpr int kKeyThreads = 288;     // bf16 rows of 576: 72 units x 4 row groups
 constexpr int kKeyBatch = 8;         // rows a thread has in flight (x 3 resident blocks: 110 KB an SM)
@@ -207,7 +209,9 @@ __global__ void __launch_bounds__(256) score_logits_simt_kernel(const T *q_abs, 
 // distributed shared memory, and the shares are then added over the heads by a
 // transposing reduction (31 shuffles for 32 columns).  The logits never leave
 // tensor memory.  The rows are 1/64 of the cache's bytes: the time is one chain
-// of load, multiply and three passes over tensor memory.
+// of load, multiply and two passes over tensor memory (64 sequences of 128
+// blocks at 128 heads: 9.8 us, 18.9 MB of means; four of 2048 blocks at 16 heads:
+// 15.3 us, eight CTAs a sequence with two tiles each).
 constexpr int kSThreads = 192;
 constexpr int kSMaxTiles = 4, kSMaxCluster = 8;
 constexpr int kSRing = 6 * 32768;      // bytes of stages: 6, 4, 3 or 2 of (1 + tiles) 16 KB chunks
@@ -433,7 +437,8 @@ __global__ void __launch_bounds__(256) score_sum_kernel(const float *logits, con
 // a bound leaves exactly k.  One scan over the threads then places the
 // winners.  The order is total (value, then the lower index), so the result
 // is the same however the threads run.  The work is a few KB a sequence: the
-// time is the launch, two dependent reads and the rounds' barriers.
+// time is the launch, two dependent reads and the rounds' barriers (64 of 2047
+// blocks: 4.5 us; 128 sequences of up to 512 blocks: 5.9 us).
 // ---------------------------------------------------------------------------
 constexpr int kSelMaxBlocks = 49152;   // 192 KB of keys
 constexpr int kSelRegs = 4;            // keys a thread holds in registers

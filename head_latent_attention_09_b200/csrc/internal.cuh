@@ -356,7 +356,7 @@ cudaError_t launch_tree_attn_simt(const AttnArgs &a, int P, bool fp32, cudaStrea
 cudaError_t launch_combine(const mla_config &cfg, const char *ws, const WsLayout &L, int B,
                            void *ctx_lat, float *lse, cudaStream_t s, bool out_f32 = false);
 // Tree attention: merge of the groups that are split between shares, straight
-// into the outputs (in P x gang x group_rows warps; the others are there already).
+// into the outputs (the others are there already).
 cudaError_t launch_tree_combine(const AttnArgs &a, int P, bool fp32, cudaStream_t s);
 // Accepted path of a drafted tree: row ctx_len[b] + path[b, i] of the cache
 // moves to ctx_len[b] + i, i < n_path[b]; new_len[b] = ctx_len[b] + n_path[b].

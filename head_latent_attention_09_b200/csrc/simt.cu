@@ -166,9 +166,10 @@ __device__ __forceinline__ uint4 finite_or_zero(uint4 v) {
 
 // Tree: block 0 makes the plan while the others copy the blocks that hold
 // drafted tokens, kCopyBlocks blocks of kCopyRows rows per sequence (rows of
-// 72 16-byte units).  (The plan made in line, with the attention kernel waiting
-// for the copy only where it reads it, saved 0.7 us of 25 on one short sequence
-// and cost 2 % on long ones, whose kernel then spilled registers.)
+// 72 16-byte units).  At most 147 KB a sequence, so the time is that of the
+// launch and of two dependent reads.  (The plan made in line, with the attention
+// kernel waiting for the copy only where it reads it, saved 0.7 us of 25 on one
+// short sequence and cost 2 % on long ones, whose kernel then spilled registers.)
 constexpr int kCopyRows = 8, kCopyBlocks = kTreeCopyRows / kCopyRows;
 __global__ void __launch_bounds__(1024) tree_plan_copy_kernel(PlanSource src, AttnArgs a, int P_req, long long cap) {
   pdl_trigger();

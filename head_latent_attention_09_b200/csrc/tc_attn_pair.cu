@@ -22,14 +22,27 @@
 // column-split for O -- which raises L2->SM traffic but reads HBM once and
 // needs no exchange of partial scores between the SMs.
 //
-// Why 256-token tiles: one thread issues the MMAs, and back-to-back
-// tcgen05.mma instructions cost ~55 cycles each however little work they
-// carry; a pair MMA with N = 256 carries 64 cycles of work, so only N = 256
-// keeps the tensor pipe busy.  A 256-token tile does not fit in shared memory
-// beside the resident query (72 KB), so it is streamed: S = Q K^T in nine
+// Why 256-token tiles: one thread issues the MMAs, and a tcgen05.mma takes at
+// least 45 cycles however little work it carries (measured); a pair MMA of
+// M = 128 has the tensor pipe's full rate at N = 256 (64 cycles), not at
+// N = 128 (45 for half the work).  A 256-token tile does not fit in shared
+// memory beside the resident query (72 KB), so it is streamed: S = Q K^T in nine
 // chunks of 64 columns (this CTA's 128 tokens, 16 KB each), O += P V in eight
 // sub-stages of 64 tokens x 128 columns (16 KB each), all through one ring of
 // 16 KB slots filled in the order the MMAs consume them.
+//
+// The roles that issue (TMA, MMA) run in a thread that elect.sync picks: with
+// the thread picked by its lane number a wait, four MMAs and a commit took 493
+// cycles instead of 257, which is the MMAs' own time.
+//
+// What bounds it: one call of a tree runs at 1.15 to 1.26 PFLOP/s (16 sequences
+// of 8192 tokens x 1024 query rows 252 us; two of 12 to 16 thousand x 8192 rows
+// 400 us), where the MMAs wait for ring slots (16 KB from L2 per 256 cycles and
+// SM, seven in flight); back to back the board's power limit takes the clock to
+// 1450-1700 MHz and the rate to 1.0-1.1 PFLOP/s.  Decode attention (128 rows a
+// sequence, 64 x 8192 tokens: 153 us, 3.9 TB/s) adds the pieces' boundaries and
+// its start of some 8 us; 2048 selected tokens of each of 64 sequences take 59
+// us, 2.6 TB/s, nearly half of it boundaries and start.
 //
 // Warp roles per CTA (352 threads): warp 0 TMA producer, warp 1
 // tensor-memory allocation and (leader CTA only) MMA issue, warps 2-9 softmax,
@@ -40,8 +53,8 @@
 // token, head), any number of them, cut into groups of 128; a group takes the
 // place of the 128 heads of one sequence and walks the cached tokens and the
 // drafted ones behind them.  Only tiles that reach past the cached tokens look
-// at the mask: a row's validity for its 128 columns is four 32-bit words built
-// from its 64-bit mask by shifts.  P.V takes the one or two blocks that hold
+// at the mask: the validity of a thread's 64 columns is two 32-bit words built
+// from the row's 64-bit mask by shifts.  P.V takes the one or two blocks that hold
 // drafted tokens (and the zeros behind them) from a copy that the plan's
 // launch made, with non-finite values replaced by zero: a masked token has
 // probability 0, but 0 * NaN would reach every row of the tile (a row that
@@ -341,13 +354,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // --------------------------------------------------------------- producer
     // Fills the ring in the order the MMAs consume it: the nine K chunks of
     // tile i, then the V sub-stages of tile i-1; at the end of a piece its last
-    // tile's V comes before the next piece's K, which waits for another Q.  A slot's full barrier (the leader's) takes an arrival
-    // from each CTA; the leader's also arms it with the bytes both CTAs' loads
-    // bring (the peer's loads count on the leader's barrier directly).  One
-    // elected thread does it all, in few instructions a slot (the MMAs want
-    // one every 256 cycles): a tile's four cache rows are looked up once, for
-    // the tile after the one being loaded, so that a paged cache's table reads
-    // are not waited for.
+    // tile's V comes before the next piece's K, which waits for another Q.  A
+    // slot's full barrier (the leader's) takes an arrival from each CTA; the
+    // leader's also arms it with the bytes both CTAs' loads bring (the peer's
+    // loads count on the leader's barrier directly).  One elected thread does it
+    // all, in few instructions a slot (the MMAs want one every 256 cycles): a
+    // tile's four cache rows are looked up once, for the tile after the one being
+    // loaded, so that a paged cache's table reads are not waited for.
     if (ptx::elect_one()) {
       const bool boxes64 = a.page_size != 0 || (!kTree && a.sel != nullptr);
       const uint32_t lq = ptx::leader_addr(bars.qfull());

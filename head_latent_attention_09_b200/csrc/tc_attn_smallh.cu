@@ -8,10 +8,17 @@
 //   S^T = K Q^T      M = 128 tokens, N = n_h heads, K = 576 (nine 64-col chunks)
 //   O^T += V^T P^T   M = 128 latent columns per MMA (four blocks), N = n_h,
 //                    K = 128 tokens
-// A tcgen05.mma instruction takes at least ~124 cycles however little it
-// computes (measured), so this path is bound by the number of MMA
-// instructions per cached token: M = 128 needs 68 per 128 tokens, half of
-// what M = 64 needs.
+// A tcgen05.mma instruction takes at least 45 cycles however little it computes
+// (measured), and M = 128 needs 68 per 128 tokens, half of what M = 64 needs:
+// 1.6 us a tile, less than the 3.3 us in which HBM brings the 147 KB of a tile
+// to every SM.  (They are issued by a thread that elect.sync picks; picked by
+// its lane number the issue alone took 4.3 us a tile.)
+//
+// What bounds it: HBM with the chain of a tile beside it, 4.3 us a tile in long
+// contexts (16 heads, 4 x 131072 tokens: 121 us, 5.0 TB/s; 32 x 4096: 40 us); in
+// short ones (one tile a CTA, as with 64 selected blocks of four sequences: 17
+// us) the chain alone, of which code that runs once and is fetched as it runs
+// took microseconds: reductions and epilogue are kept short for that.
 //
 // A 128-token tile of the cache is read from HBM once, as nine 16 KB chunks
 // (128 rows x 64 columns): the rotary chunk into a ring of its own (it only
@@ -69,9 +76,9 @@ struct Cfg {
   // than four).
   static constexpr int kConvWarps = F8 ? 6 : 0;
   // bf16: a second TMA producer, warp 6 (the rotary chunk and latent pairs
-  // 2-3 of every tile; warp 0 the query and pairs 0-1).  A thread issuing
-  // cp.async.bulk.tensor copies sustains about two per microsecond, and a
-  // paged tile takes 18 of them (two 64-token pages x nine chunks).
+  // 2-3 of every tile; warp 0 the query and pairs 0-1).  A thread that waits
+  // for a slot and issues a copy takes some 350 cycles for both, and a paged
+  // tile has 18 copies (two 64-token pages x nine chunks).
   static constexpr int kProducers = F8 ? 1 : 2;
   static constexpr int kProd1Warp = 6;
   static constexpr int kThreads = 192 + 32 * kConvWarps + 32 * (kProducers - 1);

@@ -424,3 +424,10 @@ def test_scores_that_overflow_to_minus_infinity(sh, ctx):
             bo, bl = attention_bounds(sh, q, mine, scale, want, lse)
             within(got[0][b, k], want, bo, f"ctx_lat of sequence {b}, token {k}")
             within(got[1][b, k], lse, bl, f"lse of sequence {b}, token {k}")
+
+
+@pytest.mark.parametrize("ctx,T,parts", [((12000,), 3, 0), ((9600, 9500), 64, 600), ((2600,), 5, 45)])
+def test_rows_cut_into_more_pieces_than_a_warp_has_lanes(ctx, T, parts):
+    sh = shape(LITE) if ctx != (2600,) else shape(TINY)
+    t = Tree(sh, ctx, T, 4)
+    t.check(t.run(parts))
