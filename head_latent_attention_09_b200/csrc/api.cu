@@ -8,7 +8,7 @@
 
 #include <nvtx3/nvToolsExt.h>
 
-#include "internal.cuh"
+#include "plan.cuh"
 
 using namespace mla;
 
@@ -327,7 +327,7 @@ int decode_attn(mla_handle *h, const void *q_abs, const void *cache, const float
   // The tensor-core kernels plan for themselves, up to kInlineSeqs sequences
   // (the one for 32 heads over an FP8 cache has no shared memory left for it).
   const auto plan = [&] { return launch_plan(src, B, P, cap, tile, (char *)workspace, L, h->d_status, s); };
-  a.inline_plan = B <= kInlineSeqs && !(kv_scale && c.n_h > 16);
+  a.inline_plan = plan_fits(src, B, P, cap, tile) && !(kv_scale && c.n_h > 16);
   const Before before = a.inline_plan ? Before() : Before(plan);
   cudaError_t e = cudaErrorNotSupported;
   if (h->attn_kind == kAttnTcPair && !kv_scale && aligned16(q_abs) && aligned16(cache))

@@ -17,9 +17,10 @@ __device__ __forceinline__ bool plan_from0(const PlanSource &src) { return src.d
 // kTile, drafted tokens past the cap, a count of selected blocks that the
 // sequence does not have: each is flagged and clamped, and the tiles and every
 // attention kernel use the clamped values.
+template <bool kTree>   // kTree: `runs` and `drafted` may be set
 __device__ __forceinline__ void plan_entry(const PlanSource &src, int b, long long cap, unsigned *status, int *end_out,
                                            int *second_out) {
-  const int seq = src.runs > 1 ? b / src.runs : b;
+  const int seq = kTree && src.runs > 1 ? b / src.runs : b;
   long long n = src.sel ? src.n_sel[seq] : 0;
   long long c = src.ctx_len[seq];
   bool bad = c < 0 || c > cap;
@@ -36,7 +37,7 @@ __device__ __forceinline__ void plan_entry(const PlanSource &src, int b, long lo
       const long long last = src.sel[(long long)seq * src.sel_k + n - 1];
       if (last >= 0 && last * kTile < c) end -= max(0ll, (last + 1) * kTile - c);   // the partial block
     }
-  } else if (src.drafted > 0) {
+  } else if (kTree && src.drafted > 0) {
     end = c + src.drafted;
     if (end > cap) {
       bad = true;
@@ -74,52 +75,60 @@ __device__ __forceinline__ int plan_first(const long long *tp, int B, long long 
   return lo;
 }
 
+// Exclusive prefix over a warp's lanes, and the total.
+__device__ __forceinline__ unsigned lanes_before(unsigned x, unsigned *total) {
+  unsigned s = x;
+#pragma unroll 1
+  for (int d = 1; d < 32; d <<= 1) {
+    const unsigned y = __shfl_up_sync(0xffffffffu, s, d);
+    if ((int)(threadIdx.x & 31) >= d) s += y;
+  }
+  *total = __shfl_sync(0xffffffffu, s, 31);
+  return s - x;
+}
+
 // Makes the plan for P_req shares in `o` (every thread of the CTA, which works
-// on share `share`); block 0 stores it in the workspace.
+// on share `share`); block 0 stores it in the workspace.  The caller has made
+// sure that tiles x shares fits 32 bits (plan_fits): this code runs once per CTA
+// and its instructions are fetched as it runs, so it is kept short (in 64 bits
+// and unrolled the scans took 10100 cycles, so 2700 for 64 sequences, 2300 for
+// four; the two dependent reads of the lengths before them 1600 to 2700).
 __device__ __forceinline__ void plan_in_line(const AttnArgs &a, int share, int P_req, PlanSmem &o) {
   const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31;
-  const bool from0 = plan_from0(a.src);
+#pragma unroll 1
   for (int b = tid; b < a.B; b += nt) {
     int end, second;
-    plan_entry(a.src, b, a.cap, a.status, &end, &second);
+    plan_entry<false>(a.src, b, a.cap, a.status, &end, &second);
     o.ends[b] = end;
     o.seconds[b] = second;
-    o.pb[b] = ((unsigned)(end - (from0 ? 0 : second)) + (unsigned)a.plan_tile - 1u) / (unsigned)a.plan_tile;   // tiles
+    o.pb[b] = ((unsigned)(end - (a.src.sel ? 0 : second)) + (unsigned)a.plan_tile - 1u) / (unsigned)a.plan_tile;   // tiles
   }
   __syncthreads();
   if (tid < 32) {
     const int per = (a.B + 31) / 32, b0 = min(a.B, lane * per), b1 = min(a.B, b0 + per);
-    auto before = [&](long long x, long long *total) {   // exclusive prefix over the lanes
-      long long s = x;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, s, d);
-        if (lane >= d) s += y;
-      }
-      *total = __shfl_sync(0xffffffffu, s, 31);
-      return s - x;
-    };
-    long long sum = 0, Ttot, pieces;
-    for (int b = b0; b < b1; ++b) sum += o.pb[b];
-    long long run = before(sum, &Ttot);
+    unsigned sum = 0, Ttot, pieces;
+#pragma unroll 1
+    for (int b = b0; b < b1; ++b) sum += (unsigned)o.pb[b];
+    unsigned run = lanes_before(sum, &Ttot);
+    const unsigned P = min(Ttot, (unsigned)P_req);
+    const unsigned mine = (unsigned)share < P ? (unsigned)share * Ttot / P : 0xffffffffu;   // this share's first tile
+    sum = 0;
+#pragma unroll 1
     for (int b = b0; b < b1; ++b) {
+      const unsigned t = (unsigned)o.pb[b];
       o.tp[b] = run;
-      run += o.pb[b];
-    }
-    const long long P = Ttot < (long long)P_req ? Ttot : (long long)P_req;
-    long long np = 0;
-    for (int b = b0; b < b1; ++b) {
-      const long long t = o.pb[b];
-      const long long n =
-          t > 0 ? plan_share_of_tile(o.tp[b] + t - 1, P, Ttot) - plan_share_of_tile(o.tp[b], P, Ttot) + 1 : 0;
+      const unsigned n = t > 0 ? ((run + t) * P - 1u) / Ttot - ((run + 1u) * P - 1u) / Ttot + 1u : 0u;
+      if (mine - run < t) o.first = b;
       o.pb[b] = n;
-      np += n;
+      run += t;
+      sum += n;
     }
-    long long prun = before(np, &pieces);
+    run = lanes_before(sum, &pieces);
+#pragma unroll 1
     for (int b = b0; b < b1; ++b) {
-      const long long n = o.pb[b];
-      o.pb[b] = prun;
-      prun += n;
+      const unsigned n = (unsigned)o.pb[b];
+      o.pb[b] = run;
+      run += n;
     }
     if (lane == 0) {
       o.tp[a.B] = Ttot;
@@ -127,14 +136,13 @@ __device__ __forceinline__ void plan_in_line(const AttnArgs &a, int share, int P
       o.P = P;
       o.Ttot = Ttot;
     }
-    __syncwarp();
-    if (lane == 0 && share < P) o.first = plan_first(o.tp, a.B, share, P, Ttot);
   }
   __syncthreads();
-  if (blockIdx.x == 0) {
+  if (blockIdx.x == 0) {   // for the merge (which needs no share_first)
     long long *tp = reinterpret_cast<long long *>(a.ws + a.L.tile_prefix_off);
     long long *pb = reinterpret_cast<long long *>(a.ws + a.L.piece_base_off);
-    int *ends = reinterpret_cast<int *>(a.ws + a.L.ctx_off), *first = reinterpret_cast<int *>(a.ws + a.L.share_first_off);
+    int *ends = reinterpret_cast<int *>(a.ws + a.L.ctx_off);
+#pragma unroll 1
     for (int b = tid; b <= a.B; b += nt) {
       tp[b] = o.tp[b];
       pb[b] = o.pb[b];
@@ -143,7 +151,6 @@ __device__ __forceinline__ void plan_in_line(const AttnArgs &a, int share, int P
         ends[a.B + b] = o.seconds[b];
       }
     }
-    for (int w = tid; w < o.P; w += nt) first[w] = plan_first(o.tp, a.B, w, o.P, o.Ttot);
     if (tid == 0) {
       WsHeader *hd = reinterpret_cast<WsHeader *>(a.ws);
       hd->B = a.B;
@@ -152,6 +159,13 @@ __device__ __forceinline__ void plan_in_line(const AttnArgs &a, int share, int P
       hd->n_pieces = o.pb[a.B];
     }
   }
+}
+
+// Whether plan_in_line can make the plan: at most kInlineSeqs sequences, and
+// tiles x shares in 32 bits whatever the lengths.
+inline bool plan_fits(const PlanSource &src, int B, int P_req, long long cap, int tile) {
+  const long long most = src.sel ? std::min(cap, (long long)src.sel_k * kTile) : cap;
+  return B <= kInlineSeqs && (double)B * (double)ceil_div_ll(most, tile) * ((double)P_req + 1.0) < 4e9;
 }
 
 }  // namespace mla

@@ -90,7 +90,7 @@ __device__ void make_plan(const PlanSource &src, int B, int P_req, long long cap
   long long local = 0;
   for (int b = b0; b < b1; ++b) {
     int end, second;
-    plan_entry(src, b, cap, status, &end, &second);
+    plan_entry<true>(src, b, cap, status, &end, &second);
     ctx_eff[b] = end;
     beg_eff[b] = second;
     const long long t = ceil_div_ll(end - (plan_from0(src) ? 0 : second), tile);

@@ -414,3 +414,41 @@ def test_block_scores_of_nan_and_of_minus_infinity(sh, at):
     assert (got[0, at] == 0).all()
     compare_scores(sh, got[:1, rest], q[:1], keys[:1, rest], [64 * len(rest)])
     compare_scores(sh, got[1:], q[1:], keys[1:], ctx[1:])
+
+
+@pytest.mark.parametrize("sh", [shape(LITE), shape(V2)])
+@pytest.mark.parametrize("B,k", [(256, 3), (257, 3), (33, 1)])
+def test_sparse_plan_in_line_and_by_its_own_kernel(sh, B, k):
+    """Up to 256 sequences the attention kernel makes the plan itself."""
+    rng = np.random.default_rng(B)
+    D, n_h = sh["d_c"] + sh["d_r"], sh["n_h"]
+    ctx = [int(c) for c in rng.integers(0, 400, B)]
+    ctx[5], ctx[6] = 0, 64
+    rows = [stored(sh, rng.standard_normal((n, D))) for n in ctx]
+    h = handle(sh)
+    cache = Cache(sh, rows, 400, 0, rng)
+    sel, n_sel = np.full((B, k), -1), np.zeros(B)
+    for b, n in enumerate(ctx):
+        blocks = -(-n // 64)
+        take = sorted(rng.permutation(blocks)[:k])
+        sel[b, :len(take)], n_sel[b] = take, len(take)
+    q = stored(sh, rng.standard_normal((B, n_h, D)) * 0.7)
+    for parts in (0, 7):
+        ws = torch.empty(M.mla_decode_workspace_size(h, B, parts), dtype=torch.uint8, device="cuda")
+        out, lse = torch.empty(B, n_h, sh["d_c"], dtype=torch_type(sh), device="cuda"), torch.empty(B, n_h, device="cuda")
+        M.mla_decode_attn_sparse(h, dev(sh, q), *cache.args, ints(ctx), ints(sel), ints(n_sel), k, B, parts, ws, ws.numel())
+        M.mla_combine_splits(h, ws, ws.numel(), B, parts, out, lse)
+        ok(h)
+        got, got_lse = host(out), host(lse)
+        for b in range(B):
+            mine = [rows[b][64 * j:64 * j + 64] for j in sel[b] if j >= 0]
+            if not mine:
+                assert (got[b] == 0).all() and np.isneginf(got_lse[b]).all()
+                continue
+            mine, qb = np.concatenate(mine).astype(np.float64), q[b].astype(np.float64)
+            scale = O.softmax_scale(sh["d_h"], sh["d_r"])
+            want, wl = O.latent_attention(qb, mine, d_c=sh["d_c"], scale=scale)
+            bo, bl = attention_bounds(sh, qb, mine, scale, want, wl)
+            within(got[b], want, bo, f"ctx_lat of sequence {b}")
+            within(got_lse[b], wl, bl, f"lse of sequence {b}")
+    M.mla_destroy(h)
