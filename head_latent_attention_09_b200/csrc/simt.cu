@@ -198,7 +198,12 @@ __global__ void __launch_bounds__(1024) tree_plan_copy_kernel(PlanSource src, At
 }
 
 // ---------------------------------------------------------------------------
-// generic attention: one warp per head, lanes split the row's features
+// generic attention: one warp per head, lanes split the row's features; kBatch
+// tokens at a time, their loads in flight together, their products summed by one
+// transposing reduction and each exponential taken by one lane.  Bound by that
+// chain of loads, shuffles and sums: a token at a time waited for its own loads
+// (float32, 4 heads x 144 columns, 16 blocks of each of four sequences: 47 us a
+// call, in batches of 16 15 us).
 // ---------------------------------------------------------------------------
 constexpr int kSimtMaxD = 576;      // d_c + d_r
 constexpr int kSimtMaxC = 512;      // d_c
@@ -218,8 +223,12 @@ __device__ __forceinline__ int fp8_group_of(int f, int d_c) {
 // scales (else elements of type T).  Tree: plan sequence b holds the heads of
 // one drafted token (b / T its batch sequence, b % T the token); a drafted
 // token that is masked is skipped, so whatever its row holds reaches nothing.
-template <typename T, bool F8, bool kTree>
+template <typename T, bool F8, bool kTree, int kQ>
 __global__ void __launch_bounds__(256) attn_simt_kernel(AttnArgs a) {
+  pdl_trigger();
+  pdl_wait();
+  constexpr int kO = kQ < kOPerLane ? kQ : kOPerLane;
+  constexpr int kBatch = kQ <= 6 ? 16 : 4;
   const WsHeader *hd = reinterpret_cast<const WsHeader *>(a.ws);
   const long long P = hd->P, Ttot = hd->Ttot;
   const int w = blockIdx.x;
@@ -252,51 +261,79 @@ __global__ void __launch_bounds__(256) attn_simt_kernel(AttnArgs a) {
     const int cached = kTree || a.sel ? plan_seconds(a)[b] : 0;
     const unsigned long long bits = kTree ? a.tree.mask[b] : 0ull;
 
-    float q[kQPerLane];
+    float q[kQ];
 #pragma unroll
-    for (int j = 0; j < kQPerLane; ++j) {
+    for (int j = 0; j < kQ; ++j) {
       const int f = lane + 32 * j;
       q[j] = f < D ? to_f(qg[((long long)b * a.n_h + h) * D + f]) : 0.f;
     }
-    float o[kOPerLane];
+    float o[kO];
 #pragma unroll
-    for (int j = 0; j < kOPerLane; ++j) o[j] = 0.f;
+    for (int j = 0; j < kO; ++j) o[j] = 0.f;
     float m = -CUDART_INF_F, l = 0.f;
 
-    for (long long p = p_begin; p < p_end; ++p) {
-      if (kTree && p >= cached && !((bits >> (p - cached)) & 1ull)) continue;
-      const long long row = a.sel ? selected_row(a, b, p, ctx, cached) : token_row(a, seq, p);
-      if (row < 0) {
-        if (lane == 0) atomicOr(a.status, kStatusBounds);
-        continue;
+    for (long long p0 = p_begin; p0 < p_end; p0 += kBatch) {
+      // lane t looks up token t of the batch; -1: masked, past the piece or not there
+      long long mine = -1;
+      const long long p = p0 + lane;
+      if (lane < kBatch && p < p_end && !(kTree && p >= cached && !((bits >> (p - cached)) & 1ull))) {
+        mine = a.sel ? selected_row(a, b, p, ctx, cached) : token_row(a, seq, p);
+        if (mine < 0) atomicOr(a.status, kStatusBounds);
       }
-      float val[kQPerLane];
+      float val[kBatch][kQ], x[kBatch];
 #pragma unroll
-      for (int j = 0; j < kQPerLane; ++j) {
-        const int f = lane + 32 * j;
-        val[j] = 0.f;
-        if (f < D) {
-          if (F8) val[j] = e4m3_value(cache8[row * D + f]) * a.kv_scale[row * a.n_groups + fp8_group_of(f, a.d_c)];
-          else val[j] = to_f(cache[row * D + f]);
+      for (int t = 0; t < kBatch; ++t) {
+        const long long row = __shfl_sync(0xffffffffu, mine, t);
+#pragma unroll
+        for (int j = 0; j < kQ; ++j) {
+          const int f = lane + 32 * j;
+          val[t][j] = 0.f;
+          if (row >= 0 && f < D) {
+            if (F8) val[t][j] = e4m3_value(cache8[row * D + f]) * a.kv_scale[row * a.n_groups + fp8_group_of(f, a.d_c)];
+            else val[t][j] = to_f(cache[row * D + f]);
+          }
         }
       }
-      float part = 0.f;
 #pragma unroll
-      for (int j = 0; j < kQPerLane; ++j) part += q[j] * val[j];
-      const float s = warp_sum(part) * a.scale_log2;   // score in log2 units
-      const float m_new = fmaxf(m, s);
-      // a tree's row whose scores have all overflowed to -inf so far: -inf - -inf is NaN
-      const float m_use = kTree && m_new == -CUDART_INF_F ? 0.f : m_new;
-      const float corr = exp2f(m - m_use);
-      const float pr = exp2f(s - m_use);
-      l = l * corr + pr;
+      for (int t = 0; t < kBatch; ++t) {
+        x[t] = 0.f;
 #pragma unroll
-      for (int j = 0; j < kOPerLane; ++j) {
-        const int f = lane + 32 * j;
-        if (f < a.d_c) o[j] = o[j] * corr + pr * val[j];
+        for (int j = 0; j < kQ; ++j) x[t] += q[j] * val[t][j];
       }
-      m = m_new;
+      // Sums over the lanes, each exchange halving the tokens a lane is in charge
+      // of: lane t ends with the product of token t (mod kBatch).
+#pragma unroll
+      for (int d = kBatch / 2; d > 0; d >>= 1) {
+        const bool up = (lane & d) != 0;
+#pragma unroll
+        for (int j = 0; j < d; ++j) {
+          const float give = up ? x[j] : x[j + d], keep = up ? x[j + d] : x[j];
+          x[j] = keep + __shfl_xor_sync(0xffffffffu, give, d);
+        }
+      }
+#pragma unroll
+      for (int d = kBatch; d < 32; d <<= 1) x[0] += __shfl_xor_sync(0xffffffffu, x[0], d);
+      const bool here = __shfl_sync(0xffffffffu, mine >= 0 ? 1 : 0, lane & (kBatch - 1)) != 0;
+      const float s = here ? x[0] * a.scale_log2 : -CUDART_INF_F;   // score in log2 units
+      float top = fmaxf(m, s);
+#pragma unroll
+      for (int d = kBatch / 2; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+      // scores of -inf alone so far: -inf - -inf is NaN
+      const float m_use = top == -CUDART_INF_F ? 0.f : top;
+      const float corr = exp2f(m - m_use), pr = exp2f(s - m_use);
+      l = l * corr + (lane < kBatch ? pr : 0.f);
+#pragma unroll
+      for (int j = 0; j < kO; ++j) o[j] *= corr;
+#pragma unroll
+      for (int t = 0; t < kBatch; ++t) {
+        const float wt = __shfl_sync(0xffffffffu, pr, t);
+#pragma unroll
+        for (int j = 0; j < kO; ++j)
+          if (lane + 32 * j < a.d_c) o[j] += wt * val[t][j];
+      }
+      m = top;
     }
+    l = warp_sum(l);   // a lane's tokens so far
     if (kTree) {
       // a row that attends nothing is zero; a NaN sum stays NaN
       const TreePiece tpc = tree_piece(a, tp, b, w, 0, P, Ttot);
@@ -305,7 +342,7 @@ __global__ void __launch_bounds__(256) attn_simt_kernel(AttnArgs a) {
       const long long orow = (long long)b * a.n_h + h, prow = part_row(a.L, tpc.slot, h);
       T *out = reinterpret_cast<T *>(a.tree.out) + orow * a.d_c;
 #pragma unroll
-      for (int j = 0; j < kOPerLane; ++j) {
+      for (int j = 0; j < kO; ++j) {
         const int f = lane + 32 * j;
         if (f >= a.d_c) continue;
         if (tpc.whole) out[f] = from_f<T>(o[j] * inv);
@@ -320,7 +357,7 @@ __global__ void __launch_bounds__(256) attn_simt_kernel(AttnArgs a) {
     const float inv = l > 0.f ? 1.f / l : 0.f;
     float *dst = opart + part_row(a.L, piece, h) * (long long)a.d_c;
 #pragma unroll
-    for (int j = 0; j < kOPerLane; ++j) {
+    for (int j = 0; j < kO; ++j) {
       const int f = lane + 32 * j;
       if (f < a.d_c) dst[f] = o[j] * inv;
     }
@@ -610,25 +647,25 @@ cudaError_t launch_tree_plan_copy(const PlanSource &src, const AttnArgs &a, int 
   return launch_pdl(tree_plan_copy_kernel, dim3((unsigned)blocks), dim3(threads), 0, s, 1, src, a, P, cap);
 }
 
-cudaError_t launch_attn_simt(const AttnArgs &a, int P, bool fp32, cudaStream_t s) {
+namespace {
+template <typename T, bool F8, bool kTree>
+cudaError_t launch_simt(const AttnArgs &a, int P, cudaStream_t s) {
   if (a.d_c + a.d_r > kSimtMaxD || a.d_c > kSimtMaxC) return cudaErrorNotSupported;
   const int warps = a.n_h < 8 ? a.n_h : 8;
-  dim3 grid(P, (a.n_h + warps - 1) / warps);
-  const bool f8 = a.kv_scale != nullptr;
-  if (fp32 && f8) attn_simt_kernel<float, true, false><<<grid, warps * 32, 0, s>>>(a);
-  else if (fp32) attn_simt_kernel<float, false, false><<<grid, warps * 32, 0, s>>>(a);
-  else if (f8) attn_simt_kernel<__nv_bfloat16, true, false><<<grid, warps * 32, 0, s>>>(a);
-  else attn_simt_kernel<__nv_bfloat16, false, false><<<grid, warps * 32, 0, s>>>(a);
-  return cudaGetLastError();
+  const dim3 grid(P, (a.n_h + warps - 1) / warps);
+  // rows of up to 192 columns: six a lane, which leaves registers for longer batches
+  if (a.d_c + a.d_r <= 192) return launch_pdl(attn_simt_kernel<T, F8, kTree, 6>, grid, dim3(warps * 32), 0, s, 1, a);
+  return launch_pdl(attn_simt_kernel<T, F8, kTree, kQPerLane>, grid, dim3(warps * 32), 0, s, 1, a);
+}
+}  // namespace
+
+cudaError_t launch_attn_simt(const AttnArgs &a, int P, bool fp32, cudaStream_t s) {
+  if (a.kv_scale) return fp32 ? launch_simt<float, true, false>(a, P, s) : launch_simt<__nv_bfloat16, true, false>(a, P, s);
+  return fp32 ? launch_simt<float, false, false>(a, P, s) : launch_simt<__nv_bfloat16, false, false>(a, P, s);
 }
 
 cudaError_t launch_tree_attn_simt(const AttnArgs &a, int P, bool fp32, cudaStream_t s) {
-  if (a.d_c + a.d_r > kSimtMaxD || a.d_c > kSimtMaxC) return cudaErrorNotSupported;
-  const int warps = a.n_h < 8 ? a.n_h : 8;
-  dim3 grid(P, (a.n_h + warps - 1) / warps);
-  if (fp32) attn_simt_kernel<float, false, true><<<grid, warps * 32, 0, s>>>(a);
-  else attn_simt_kernel<__nv_bfloat16, false, true><<<grid, warps * 32, 0, s>>>(a);
-  return cudaGetLastError();
+  return fp32 ? launch_simt<float, false, true>(a, P, s) : launch_simt<__nv_bfloat16, false, true>(a, P, s);
 }
 
 // Vectorised combine for d_c a multiple of 4 and at most 512: `segs` warps per
