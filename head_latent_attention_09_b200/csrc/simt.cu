@@ -228,7 +228,9 @@ __global__ void __launch_bounds__(256) attn_simt_kernel(AttnArgs a) {
   pdl_trigger();
   pdl_wait();
   constexpr int kO = kQ < kOPerLane ? kQ : kOPerLane;
-  constexpr int kBatch = kQ <= 6 ? 16 : 4;
+  // long rows: two at a time keep twice the blocks resident of four (64 heads, 16
+  // x 2048 tokens 650 and 850 us; few tokens would rather have four: 42 and 35)
+  constexpr int kBatch = kQ <= 6 ? 16 : 2;
   const WsHeader *hd = reinterpret_cast<const WsHeader *>(a.ws);
   const long long P = hd->P, Ttot = hd->Ttot;
   const int w = blockIdx.x;
@@ -280,20 +282,31 @@ __global__ void __launch_bounds__(256) attn_simt_kernel(AttnArgs a) {
         mine = a.sel ? selected_row(a, b, p, ctx, cached) : token_row(a, seq, p);
         if (mine < 0) atomicOr(a.status, kStatusBounds);
       }
-      float val[kBatch][kQ], x[kBatch];
+      // every load of the batch before any conversion, which would wait for it
+      T raw[kBatch][F8 ? 1 : kQ];
+      uint8_t code[kBatch][F8 ? kQ : 1];
+      float sigma[kBatch][F8 ? kQ : 1];
 #pragma unroll
       for (int t = 0; t < kBatch; ++t) {
         const long long row = __shfl_sync(0xffffffffu, mine, t);
+        const bool there = row >= 0;
 #pragma unroll
         for (int j = 0; j < kQ; ++j) {
           const int f = lane + 32 * j;
-          val[t][j] = 0.f;
-          if (row >= 0 && f < D) {
-            if (F8) val[t][j] = e4m3_value(cache8[row * D + f]) * a.kv_scale[row * a.n_groups + fp8_group_of(f, a.d_c)];
-            else val[t][j] = to_f(cache[row * D + f]);
+          const bool ld = there && f < D;
+          if (F8) {
+            code[t][j] = ld ? cache8[row * D + f] : (uint8_t)0;
+            sigma[t][j] = ld ? a.kv_scale[row * a.n_groups + fp8_group_of(f, a.d_c)] : 0.f;
+          } else {
+            raw[t][j] = ld ? cache[row * D + f] : from_f<T>(0.f);
           }
         }
       }
+      float val[kBatch][kQ], x[kBatch];
+#pragma unroll
+      for (int t = 0; t < kBatch; ++t)
+#pragma unroll
+        for (int j = 0; j < kQ; ++j) val[t][j] = F8 ? e4m3_value(code[t][F8 ? j : 0]) * sigma[t][F8 ? j : 0] : to_f(raw[t][F8 ? 0 : j]);
 #pragma unroll
       for (int t = 0; t < kBatch; ++t) {
         x[t] = 0.f;
