@@ -35,14 +35,14 @@
 // the thread picked by its lane number a wait, four MMAs and a commit took 493
 // cycles instead of 257, which is the MMAs' own time.
 //
-// What bounds it: one call of a tree runs at 1.15 to 1.26 PFLOP/s (16 sequences
-// of 8192 tokens x 1024 query rows 252 us; two of 12 to 16 thousand x 8192 rows
-// 400 us), where the MMAs wait for ring slots (16 KB from L2 per 256 cycles and
+// What bounds it: one call of a tree runs at 1.17 to 1.28 PFLOP/s (16 sequences
+// of 8192 tokens x 1024 query rows 248 us; two of 12 to 16 thousand x 8192 rows
+// 396 us), where the MMAs wait for ring slots (16 KB from L2 per 256 cycles and
 // SM, seven in flight); back to back the board's power limit takes the clock to
 // 1450-1700 MHz and the rate to 1.0-1.1 PFLOP/s.  Decode attention (128 rows a
-// sequence, 64 x 8192 tokens: 153 us, 3.9 TB/s) adds the pieces' boundaries and
-// its start of some 8 us; 2048 selected tokens of each of 64 sequences take 59
-// us, 2.6 TB/s, nearly half of it boundaries and start.
+// sequence, 64 x 8192 tokens: 146 us, 4.1 TB/s) adds the latency of HBM in every
+// K slot, the pieces' boundaries and a start of some 8 us; 2048 selected tokens of
+// each of 64 sequences take 56 us, 2.7 TB/s, nearly half of it boundaries and start.
 //
 // Warp roles per CTA (352 threads): warp 0 TMA producer, warp 1
 // tensor-memory allocation and (leader CTA only) MMA issue, warps 2-9 softmax,
