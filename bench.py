@@ -936,7 +936,8 @@ def run_ours(args):
             "median_frac": attn_bytes / (float(np.median(attn_samples_us)) * 1e-6) / 1e9 / hbm_peak,
             "tokens_scanned_per_s": ctx_sum / (float(np.median(attn_samples_us)) * 1e-6),
             "note": "mla_decode_attn alone, one call per event pair, after the timed region"},
-        "gpu_launches": (5 if args.fused else 6) * args.steps,
+        # up to 256 sequences the attention kernel makes the split plan itself
+        "gpu_launches": ((4 if args.fused else 5) + (1 if B > 256 else 0)) * args.steps,
         "step_calls": ("mla_cache_append, mla_absorb_q, mla_decode_attn (plan + attention), " +
                        ("mla_combine_out_proj" if args.fused else "mla_combine_splits, mla_out_proj")),
         "per_call_us": per_call,
