@@ -61,7 +61,8 @@ struct PlanSmem {
   long long tp[kInlineSeqs + 1], pb[kInlineSeqs + 1];
   int ends[kInlineSeqs], seconds[kInlineSeqs];
   long long P, Ttot;
-  int first;   // first plan sequence of this CTA's share
+  unsigned t0, t1;   // tiles of this CTA's share
+  int first;         // its first plan sequence
 };
 
 // First plan sequence whose tiles reach past the first tile of share w.
@@ -135,6 +136,8 @@ __device__ __forceinline__ void plan_in_line(const AttnArgs &a, int share, int P
       o.pb[a.B] = pieces;
       o.P = P;
       o.Ttot = Ttot;
+      o.t0 = mine;
+      o.t1 = (unsigned)share < P ? ((unsigned)share + 1u) * Ttot / P : 0u;
     }
   }
   __syncthreads();

@@ -685,7 +685,7 @@ cudaError_t launch_tree_attn_simt(const AttnArgs &a, int P, bool fp32, cudaStrea
 // (sequence, head), each for 128 / segs of every 128 float4 columns, 8 warps
 // per block.  A warp reduces the pieces' log-sum-exps across its lanes; then
 // the lanes compute the weights of 32 pieces at a time, one each, and pass them
-// round by shuffles while the loads of kMergeAhead pieces are in flight.  With
+// round by shuffles while the loads of kAhead pieces are in flight.  With
 // many rows one warp each fills the GPU; with few (long contexts split many
 // times) four warps a row and the loads in flight take the place of the missing
 // rows (4 sequences x 16 heads x 37 pieces: 32 -> 8 us).
@@ -704,20 +704,19 @@ __device__ __forceinline__ void store4<__nv_bfloat16>(__nv_bfloat16 *dst, float4
   *reinterpret_cast<uint2 *>(dst) = u;
 }
 
-constexpr int kMergeAhead = 8;
 template <typename T, int kPer>   // float4 columns of a lane: 4 (one warp a row) or 1 (four warps a row)
-__global__ void __launch_bounds__(256, 4) combine_vec_kernel(const char *ws, WsLayout L, int B, int n_h, int d_c,
+__global__ void __launch_bounds__(256, kPer == 1 ? 2 : 4) combine_vec_kernel(const char *ws, WsLayout L, int B, int n_h, int d_c,
                                                              T *ctx_lat, float *lse_out) {
   pdl_trigger();
   pdl_wait();
   constexpr int kSegs = 4 / kPer;
-  constexpr int kAhead = kMergeAhead / kPer;
+  constexpr int kAhead = kPer == 1 ? 16 : 2;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long unit = (long long)blockIdx.x * 8 + warp;
   const long long row = unit / kSegs;   // = b * n_h + h
   const int f0 = (int)(unit % kSegs) * 32 * kPer + lane;
   if (row >= (long long)B * n_h) return;
-  const int b = (int)(row / n_h), h = (int)(row % n_h);
+  const int b = (int)plan_div(row, n_h), h = (int)(row - (long long)b * n_h);
   const long long *pb = reinterpret_cast<const long long *>(ws + L.piece_base_off);
   const float *lse = reinterpret_cast<const float *>(ws + L.lse_off) + part_row(L, pb[b], h);
   const int n = (int)(pb[b + 1] - pb[b]);   // the row's pieces are consecutive

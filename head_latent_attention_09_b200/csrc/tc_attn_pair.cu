@@ -168,8 +168,8 @@ __device__ __forceinline__ void walk_init(Walk<kInl> &w, const AttnArgs &a, cons
   w.b = a.B;
   if (share >= P) return;
   w.b = kInl ? o.first : reinterpret_cast<const int *>(a.ws + a.L.share_first_off)[share];
-  w.t0 = plan_begin(share, P, Ttot);
-  w.t1 = plan_begin(share + 1, P, Ttot);
+  w.t0 = kInl ? o.t0 : plan_begin(share, P, Ttot);
+  w.t1 = kInl ? o.t1 : plan_begin(share + 1, P, Ttot);
 }
 
 // Next piece of this share; false when done.

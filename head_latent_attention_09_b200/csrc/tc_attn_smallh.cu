@@ -165,6 +165,8 @@ __device__ __forceinline__ void walk_init(Walk &w, const AttnArgs &a, const Plan
     w.seconds = o.seconds;
     if (share >= w.P) return;
     w.b = o.first;
+    w.t0 = o.t0;
+    w.t1 = o.t1;
   } else {
     const WsHeader *hd = reinterpret_cast<const WsHeader *>(a.ws);
     w.P = hd->P;
@@ -175,9 +177,9 @@ __device__ __forceinline__ void walk_init(Walk &w, const AttnArgs &a, const Plan
     w.seconds = plan_seconds(a);
     if (share >= w.P) return;
     w.b = reinterpret_cast<const int *>(a.ws + a.L.share_first_off)[share];   // found by the plan
+    w.t0 = plan_begin(share, w.P, w.Ttot);
+    w.t1 = plan_begin(share + 1, w.P, w.Ttot);
   }
-  w.t0 = plan_begin(share, w.P, w.Ttot);
-  w.t1 = plan_begin(share + 1, w.P, w.Ttot);
 }
 
 __device__ __forceinline__ bool walk_next(Walk &w, const AttnArgs &a, int share, Piece &pc) {
