@@ -688,7 +688,8 @@ cudaError_t launch_tree_attn_simt(const AttnArgs &a, int P, bool fp32, cudaStrea
 // round by shuffles while the loads of kAhead pieces are in flight.  With
 // many rows one warp each fills the GPU; with few (long contexts split many
 // times) four warps a row and the loads in flight take the place of the missing
-// rows (4 sequences x 16 heads x 37 pieces: 32 -> 8 us).
+// rows (4 sequences x 16 heads x 37 pieces: 32 -> 8 us; sixteen loads in flight
+// instead of eight took most of 3 us off that sparse attention's 20.6).
 template <typename T>
 __device__ __forceinline__ void store4(T *dst, float4 v);
 template <>

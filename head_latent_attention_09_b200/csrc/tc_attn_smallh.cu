@@ -16,7 +16,7 @@
 //
 // What bounds it: HBM with the chain of a tile beside it, 4.3 us a tile in long
 // contexts (16 heads, 4 x 131072 tokens: 121 us, 5.0 TB/s; 32 x 4096: 40 us); in
-// short ones (one tile a CTA, as with 64 selected blocks of four sequences: 16
+// short ones (one tile a CTA, as with 64 selected blocks of four sequences: 14
 // us) the chain alone, of which code that runs once and is fetched as it runs
 // took microseconds: reductions and epilogue are kept short for that.
 //
