@@ -133,3 +133,52 @@ def test_draft_verify_accept_then_sparse_decode(sh, page):
     compare(host(ctx1), want["ctx"], wl, "ctx_lat over selected blocks")
     compare(host(lse1), want["lse"], wl, "lse over selected blocks")
     compare(host(o1), want["o"], wl, "o over selected blocks")
+
+
+@pytest.mark.parametrize("sh", [shape(LITE), shape(V2)])
+def test_calls_at_the_same_time_on_two_streams(sh):
+    """One handle, two streams, workspaces of their own: every run of either call
+    gives what it gives alone, bit for bit; a block listed twice counts twice."""
+    rng = np.random.default_rng(11)
+    B, T, n, k, D, n_h, dt = 5, 7, 900, 6, 576, sh["n_h"], torch_type(sh)
+    h = handle(sh)
+    cache = dev(sh, rng.standard_normal((B, n + T, D)))
+    ctx, q = ints([n, 65, 448, 0, 701]), dev(sh, rng.standard_normal((B, T, n_h, D)) * 0.7)
+    mask = words([O.tree_bits([-1, 0, 0, 1, 3, 2, 4])] * B)
+    sel = ints([[0, 3, 3, 9, 13, 14], [0, 1, -1, -1, -1, -1], [6, 2, 5, 0, 1, 4], [-1] * k, [1, 2, 3, 4, 5, 10]])
+    n_sel = ints([6, 2, 6, 0, 6])
+    out = torch.empty(B, T, n_h, 512, dtype=dt, device="cuda")
+    out1, lse1 = torch.empty(B, n_h, 512, dtype=dt, device="cuda"), torch.empty(B, n_h, device="cuda")
+    ws = torch.empty(M.mla_tree_workspace_size(h, B, T), dtype=torch.uint8, device="cuda")
+    ws1 = torch.empty(M.mla_decode_workspace_size(h, B), dtype=torch.uint8, device="cuda")
+
+    def tree(st):
+        M.mla_tree_attn(h, q, cache, n + T, None, 0, ctx, mask, B, T, 0, out, None, ws, ws.numel(), st)
+
+    def sparse(st):
+        M.mla_decode_attn_sparse(h, q, cache, n + T, None, 0, ctx, sel, n_sel, k, B, 0, ws1, ws1.numel(), st)
+        M.mla_combine_splits(h, ws1, ws1.numel(), B, 0, out1, lse1, st)
+
+    tree(None)
+    sparse(None)
+    torch.cuda.synchronize()
+    alone, alone1, alone_lse = out.clone(), out1.clone(), lse1.clone()
+    rows = host(cache)[0].reshape(-1, D)[:960]
+    twice = np.concatenate([rows[64 * j:min(64 * j + 64, n)] for j in (0, 3, 3, 9, 13, 14)])
+    want, _ = O.latent_attention(host(q).reshape(-1, n_h, D)[0], twice, d_c=512,
+                                   scale=O.softmax_scale(sh["d_h"], sh["d_r"]))
+    wl = WORKLOADS["v2lite_b32_ctx4k"]
+    compare(host(alone1)[:1], {0: want}, wl, "ctx_lat with a block listed twice")
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        out.fill_(0)
+        out1.fill_(0)
+        torch.cuda.synchronize()
+        for _ in range(3):
+            tree(a)
+            sparse(b)
+        torch.cuda.synchronize()
+        assert torch.equal(out, alone) and torch.equal(out1, alone1) and torch.equal(lse1, alone_lse)
+    ok(h)
+    M.mla_destroy(h)
