@@ -452,3 +452,24 @@ def test_sparse_plan_in_line_and_by_its_own_kernel(sh, B, k):
             within(got[b], want, bo, f"ctx_lat of sequence {b}")
             within(got_lse[b], wl, bl, f"lse of sequence {b}")
     M.mla_destroy(h)
+
+
+@pytest.mark.parametrize("sh,page", SHAPES)
+def test_block_keys_of_many_blocks(sh, page):
+    """More blocks than the GPU has SMs: the form with fewer threads a block."""
+    rng = np.random.default_rng(page + 1)
+    D = sh["d_c"] + sh["d_r"]
+    ctx = [64 * 60, 64 * 59 + 1, 64 * 31 - 1, 200]
+    rows = [stored(sh, rng.standard_normal((n, D)) + 0.3) for n in ctx]
+    h = handle(sh, page)
+    cache = Cache(sh, rows, 64 * 60, page, rng)
+    keys = torch.full((4, 60, D), 9.0, dtype=torch_type(sh), device="cuda")
+    M.mla_block_keys(h, *cache.args, None, ints(ctx), 4, 64 * 60, keys, 60)
+    ok(h)
+    M.mla_destroy(h)
+    got = host(keys)
+    for b in range(4):
+        want, mass = O.block_means(rows[b]), O.block_means(np.abs(rows[b]))
+        assert (got[b, len(want):] == 9.0).all()
+        within(got[b, :len(want)], want, half_step(sh) * 1.01 * np.abs(want) + 65 * 2.0 ** -24 * mass,
+               f"means of sequence {b}")
