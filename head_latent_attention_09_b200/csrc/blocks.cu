@@ -160,7 +160,9 @@ cudaError_t launch_keys(const AttnArgs &a, const int *ctx_begin, const int *ctx_
 // ---------------------------------------------------------------------------
 constexpr int kScoreTile = 128;
 
-__device__ __forceinline__ int blocks_of(int ctx) { return ctx <= 0 ? 0 : (ctx + kTile - 1) / kTile; }
+// Blocks of a sequence of ctx tokens, any int: ctx + kTile - 1 would overflow near
+// 2^31 and come out negative.
+__device__ __forceinline__ int blocks_of(int ctx) { return ctx <= 0 ? 0 : (ctx - 1) / kTile + 1; }
 // log2 of the tokens in block j of a sequence of ctx tokens
 __device__ __forceinline__ float log2_tokens(int j, int ctx) {
   const int n = ctx - j * kTile;

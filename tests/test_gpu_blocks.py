@@ -473,3 +473,29 @@ def test_block_keys_of_many_blocks(sh, page):
         assert (got[b, len(want):] == 9.0).all()
         within(got[b, :len(want)], want, half_step(sh) * 1.01 * np.abs(want) + 65 * 2.0 ** -24 * mass,
                f"means of sequence {b}")
+
+
+@pytest.mark.parametrize("sh", [shape(LITE), shape(V2), shape(TINY)])
+@pytest.mark.parametrize("n", [2 ** 31 - 1, 2 ** 31 - 63, 2 ** 31 - 64, -1, -2 ** 31])
+def test_lengths_at_the_ends_of_the_integers(sh, n):
+    """Scores and selection of a length that no cache holds: flagged, and taken
+    over the blocks there are (none of a negative length); nothing is written
+    outside the outputs."""
+    rng = np.random.default_rng(0)
+    blocks, k, D = 5, 3, sh["d_c"] + sh["d_r"]
+    keys = stored(sh, rng.standard_normal((2, blocks, D)))
+    q = stored(sh, rng.standard_normal((2, sh["n_h"], D)) * 0.7)
+    ctx = [n, 64 * 4]
+    h = handle(sh)
+    got = scores_of(sh, h, q, keys, ctx, blocks)
+    assert M.mla_get_device_status(h) == M.MLA_ERR_DEVICE_BOUNDS
+    compare_scores(sh, got, q, keys, [64 * blocks if n > 0 else 0, ctx[1]])
+    guard = torch.full((2 * k + 4096,), 77, dtype=torch.int32, device="cuda")
+    sel, n_sel = guard[2048:2048 + 2 * k], ints([9, 9])
+    M.mla_block_select(h, torch.from_numpy(got.astype(np.float32)).cuda(), blocks, ints(ctx), 2, k, 0, 1, sel, n_sel)
+    assert M.mla_get_device_status(h) == M.MLA_ERR_DEVICE_BOUNDS
+    M.mla_destroy(h)
+    want = [O.block_select(got[0].tolist(), k, 0, 1) if n > 0 else [], O.block_select(got[1, :4].tolist(), k, 0, 1)]
+    assert n_sel.tolist() == [len(w) for w in want]
+    assert sel.tolist() == want[0] + [-1] * (k - len(want[0])) + want[1]
+    assert (guard[:2048] == 77).all() and (guard[2048 + 2 * k:] == 77).all()
