@@ -347,11 +347,11 @@ __global__ void __launch_bounds__(256) attn_simt_kernel(AttnArgs a) {
       m = top;
     }
     l = warp_sum(l);   // a lane's tokens so far
+    // a row that attends nothing is zero; a NaN sum stays NaN
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const float z = l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * 0.69314718055994531f;
     if (kTree) {
-      // a row that attends nothing is zero; a NaN sum stays NaN
       const TreePiece tpc = tree_piece(a, tp, b, w, 0, P, Ttot);
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-      const float z = l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * 0.69314718055994531f;
       const long long orow = (long long)b * a.n_h + h, prow = part_row(a.L, tpc.slot, h);
       T *out = reinterpret_cast<T *>(a.tree.out) + orow * a.d_c;
 #pragma unroll
@@ -367,17 +367,20 @@ __global__ void __launch_bounds__(256) attn_simt_kernel(AttnArgs a) {
       }
       continue;
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
     float *dst = opart + part_row(a.L, piece, h) * (long long)a.d_c;
 #pragma unroll
     for (int j = 0; j < kO; ++j) {
       const int f = lane + 32 * j;
       if (f < a.d_c) dst[f] = o[j] * inv;
     }
-    if (lane == 0)
-      lse[part_row(a.L, piece, h)] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -CUDART_INF_F;
+    if (lane == 0) lse[part_row(a.L, piece, h)] = z;
   }
 }
+
+// What a merge subtracts from its pieces' log-sum-exps: their maximum, or 0
+// where that is -inf (-inf - -inf is NaN).  A maximum does not show a NaN, so the
+// merges take a row for empty by its sum being 0, not by its maximum.
+__device__ __forceinline__ float merge_max(float m) { return m == -CUDART_INF_F ? 0.f : m; }
 
 // ---------------------------------------------------------------------------
 // log-sum-exp combine, generic form: one block per (sequence, head)
@@ -395,13 +398,14 @@ __global__ void __launch_bounds__(128) combine_kernel(const char *ws, WsLayout L
   float m = -CUDART_INF_F;
   for (long long p = p0; p < p1; ++p) m = fmaxf(m, lse[part_row(L, p, h)]);
   T *dst = ctx_lat + ((long long)b * n_h + h) * d_c;
-  if (m == -CUDART_INF_F) {
+  m = merge_max(m);
+  float tot = 0.f;
+  for (long long p = p0; p < p1; ++p) tot += expf(lse[part_row(L, p, h)] - m);
+  if (tot == 0.f) {
     for (int f = threadIdx.x; f < d_c; f += blockDim.x) dst[f] = from_f<T>(0.f);
     if (lse_out && threadIdx.x == 0) lse_out[(long long)b * n_h + h] = -CUDART_INF_F;
     return;
   }
-  float tot = 0.f;
-  for (long long p = p0; p < p1; ++p) tot += expf(lse[part_row(L, p, h)] - m);
   const float inv = 1.f / tot;
   for (int f = threadIdx.x; f < d_c; f += blockDim.x) {
     float acc = 0.f;
@@ -593,21 +597,21 @@ __global__ void __launch_bounds__(256) combine_outproj_simt_kernel(const char *w
     for (long long p = p0 + lane; p < p1; p += 32) m = fmaxf(m, lse[part_row(L, p, h)]);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+    m = merge_max(m);
     float tot = 0.f;
-    if (m != -CUDART_INF_F)
-      for (long long p = p0 + lane; p < p1; p += 32) tot += expf(lse[part_row(L, p, h)] - m);
+    for (long long p = p0 + lane; p < p1; p += 32) tot += expf(lse[part_row(L, p, h)] - m);
     tot = warp_sum(tot);
     if (lane == 0) {
       s_m = m;
-      s_inv = m == -CUDART_INF_F ? 0.f : 1.f / tot;
-      if (lse_out) lse_out[row] = m == -CUDART_INF_F ? -CUDART_INF_F : m + logf(tot);
+      s_inv = tot == 0.f ? 0.f : 1.f / tot;
+      if (lse_out) lse_out[row] = tot == 0.f ? -CUDART_INF_F : m + logf(tot);
     }
   }
   __syncthreads();
   const float m = s_m, inv = s_inv;
   for (int c = threadIdx.x; c < d_c; c += blockDim.x) {
     float acc = 0.f;
-    if (m != -CUDART_INF_F)
+    if (inv != 0.f)   // the row attends something
       for (long long p = p0; p < p1; ++p) {
         const float w = expf(lse[part_row(L, p, h)] - m) * inv;
         acc += w * op[part_row(L, p, h) * (long long)d_c + c];
@@ -742,16 +746,17 @@ __global__ void __launch_bounds__(256, kPer == 1 ? 2 : 4) combine_vec_kernel(con
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   T *dst = ctx_lat + row * d_c;
-  if (m == -CUDART_INF_F) {
+  m = merge_max(m);
+  float tot = lane < n ? expf(l0 - m) : 0.f;
+  for (int p = 32 + lane; p < n; p += 32) tot += expf(lse[p] - m);
+  tot = warp_sum(tot);
+  if (tot == 0.f) {
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
       if (f0 + 32 * i < n4) store4<T>(dst + 4 * (f0 + 32 * i), make_float4(0.f, 0.f, 0.f, 0.f));
     if (lse_out && f0 == 0) lse_out[row] = -CUDART_INF_F;
     return;
   }
-  float tot = lane < n ? expf(l0 - m) : 0.f;
-  for (int p = 32 + lane; p < n; p += 32) tot += expf(lse[p] - m);
-  tot = warp_sum(tot);
   const float inv = 1.f / tot;
   float4 acc[kPer];
 #pragma unroll
@@ -828,14 +833,15 @@ __global__ void __launch_bounds__(256) merge_ranges_kernel(const float *parts, c
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   T *dst = ctx_lat + row * d_c;
-  if (m == -CUDART_INF_F) {
+  m = merge_max(m);
+  float tot = 0.f;
+  for (int r = lane; r < R; r += 32) tot += expf(lse_parts[r * rows + row] - m);
+  tot = warp_sum(tot);
+  if (tot == 0.f) {
     for (int f = lane; f < d_c; f += 32) dst[f] = from_f<T>(0.f);
     if (lse_out && lane == 0) lse_out[row] = -CUDART_INF_F;
     return;
   }
-  float tot = 0.f;
-  for (int r = lane; r < R; r += 32) tot += expf(lse_parts[r * rows + row] - m);
-  tot = warp_sum(tot);
   const float inv = 1.f / tot;
   for (int f = lane; f < d_c; f += 32) {
     float acc = 0.f;

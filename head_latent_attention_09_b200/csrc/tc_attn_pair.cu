@@ -733,8 +733,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (!warp_wait(bars.odone((i - 1) & 1), ((i - 1) >> 1) & 1, a.status, abort_flag)) { ok = false; break; }
       ptx::tc_fence_after();
       const int head = 64 * (int)rank + h;
-      // a tree's row that attends nothing is zero, a NaN sum stays NaN
-      const bool some = kTree ? lsum != 0.f : lsum > 0.f;
+      // a row that attends nothing is zero, a NaN sum stays NaN
+      const bool some = lsum != 0.f;
       const float inv = some ? 1.f / lsum : 0.f;
       const float z = some ? (m_run + log2f(lsum)) * 0.69314718055994531f : -CUDART_INF_F;
       long long slot = pc.piece;

@@ -739,9 +739,10 @@ __global__ void __launch_bounds__(Cfg<H, F8>::kThreads, 1)
       if (lane == 0) ptx::mbar_arrive(bar + C::bLsum);
       if (!warp_wait(bar + C::bLsum, npc & 1, a.status, abort_flag)) { ok = false; break; }
       const float l = red_s[hl] + red_s[H + hl] + red_s[2 * H + hl] + red_s[3 * H + hl];
-      const float inv = l > 0.f ? 1.f / l : 0.f;
+      // a row that attends nothing is zero, a NaN sum stays NaN
+      const float inv = l != 0.f ? 1.f / l : 0.f;
       if (q == 0 && lane < H)
-        lse_out[part_row(a.L, pc.piece, lane)] = l > 0.f ? (m_run + log2f(l)) * 0.69314718055994531f : -CUDART_INF_F;
+        lse_out[part_row(a.L, pc.piece, lane)] = l != 0.f ? (m_run + log2f(l)) * 0.69314718055994531f : -CUDART_INF_F;
       if (!warp_wait(bar + C::bODone + ((i - 1) & 1), ((i - 1) >> 1) & 1, a.status, abort_flag)) { ok = false; break; }
       ptx::tc_fence_after();
       float *dst = opart + part_row(a.L, pc.piece, 0) * (long long)a.d_c + row;

@@ -142,14 +142,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (long long p = p0[j] + 32 + lane; p < p1[j]; p += 32) m = fmaxf(m, lse[part_row(g.L, p, z)]);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      const bool empty = m == -CUDART_INF_F;
+      if (m == -CUDART_INF_F) m = 0.f;   // -inf - -inf is NaN
       float tot = 0.f;
-      if (!empty) {
-        if (p0[j] + lane < p1[j]) tot += expf(l0[j] - m);
-        for (long long p = p0[j] + 32 + lane; p < p1[j]; p += 32) tot += expf(lse[part_row(g.L, p, z)] - m);
-      }
+      if (p0[j] + lane < p1[j]) tot += expf(l0[j] - m);
+      for (long long p = p0[j] + 32 + lane; p < p1[j]; p += 32) tot += expf(lse[part_row(g.L, p, z)] - m);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
+      const bool empty = tot == 0.f;     // not by the maximum, which does not show a NaN
       const int r = warp + kWarps * j, n = n0 + r;
       mx[j] = m;
       inv[j] = empty ? 0.f : 1.f / tot;
