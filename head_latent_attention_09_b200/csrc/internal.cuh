@@ -306,6 +306,11 @@ cudaError_t launch_plan(const PlanSource &src, int B, int P, long long cap, int 
 // of the blocks that hold drafted tokens.
 cudaError_t launch_tree_plan_copy(const PlanSource &src, const AttnArgs &a, int P, long long cap, cudaStream_t s);
 
+// Running maximum of a row that nothing has reached yet: the lowest finite value
+// instead of -inf, so that scores of -inf (masked, or overflowed) subtract it
+// without a NaN (-inf - -inf) and come out as 2^-inf = 0.
+constexpr float kNoMax = -3.402823466e38f;
+
 // The plan stores two values per plan sequence: the end of its attended tokens
 // (clamped), and its first token (a multiple of kTile), or for selected blocks
 // and trees, which start at token 0, the number of its cached tokens.

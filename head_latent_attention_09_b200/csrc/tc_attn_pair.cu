@@ -619,7 +619,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     int i = 0, npc_s = 0;
     bool ok = true;
     while (ok && walk_next<kTree, kInl>(w, a, share, pc)) {
-      float m_run = -CUDART_INF_F, l_part = 0.f;
+      float m_run = kNoMax, l_part = 0.f;
       // tree: this thread's query row of the sequence, and its drafted tokens
       const int row = 128 * pc.g + 64 * (int)rank + h;
       unsigned long long bits = 0ull;
@@ -664,7 +664,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         bool rescale = false;
         float alpha = 1.f;
         if (m_tile > m_run + kRescale) {
-          alpha = exp2f(m_run - m_tile);       // 0 when m_run = -inf
+          alpha = exp2f(m_run - m_tile);       // 0 when m_run = kNoMax
           m_run = m_tile;
           l_part *= alpha;
           rescale = k > 0;
@@ -673,11 +673,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // previous tile's P.V, so that only the store below waits for it.
         // P is rounded to bf16 because the MMA takes both operands in one
         // 16-bit type and V is bf16; the sum is of the unrounded values.
-        // A row with nothing valid so far (a tree's masks) subtracts 0: -inf - -inf is NaN.
-        const float m_use = kTree && m_run == -CUDART_INF_F ? 0.f : m_run;
         uint32_t pk[32];
         float2 ps[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
-        const float2 scale2 = {a.scale_log2, a.scale_log2}, m2 = {-m_use, -m_use};
+        const float2 scale2 = {a.scale_log2, a.scale_log2}, m2 = {-m_run, -m_run};
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
           float2 p = ptx::fma2({v[2 * j], v[2 * j + 1]}, scale2, m2);

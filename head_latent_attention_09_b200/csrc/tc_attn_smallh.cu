@@ -649,7 +649,7 @@ __global__ void __launch_bounds__(Cfg<H, F8>::kThreads, 1)
       // maximum here, the sum and its reciprocal at the end; l_part[hh] is this
       // token row's own share of head hh's sum.
       const int hl = lane & (H - 1);
-      float m_run = -CUDART_INF_F, l_part[H];
+      float m_run = kNoMax, l_part[H];
 #pragma unroll
       for (int hh = 0; hh < H; ++hh) l_part[hh] = 0.f;
       for (int k = 0; k < pc.ntiles; ++k, ++i) {

@@ -56,7 +56,7 @@
  *   - A sequence with ctx_len = 0 produces a zero ctx_lat row and lse = -inf.
  *   - A score that is NaN (a NaN in the query or in an attended row) or that
  *     overflows float32 to +inf makes its row of ctx_lat and its lse NaN, however
- *     the tokens are split.
+ *     the tokens are split.  One that overflows to -inf draws nothing.
  *   - Results are deterministic for a fixed num_parts (no floating-point atomics).
  *   - A handle may be used from one host thread at a time.
  */

@@ -6,7 +6,9 @@ import pytest
 import torch
 
 import head_latent_attention_09_b200 as M
-from tests.operators_harness import LITE, TINY, V2, Cache, dev, handle, host, ints, ok, shape, stored, torch_type
+from oracle import mla_oracle as O
+from tests.operators_harness import (LITE, TINY, V2, Cache, attention_bounds, dev, handle, host, ints, ok, shape, stored,
+                                     torch_type, within)
 from tests.test_gpu_blocks import Sparse
 
 pytestmark = pytest.mark.gpu
@@ -156,3 +158,29 @@ def test_fp8_attention_keeps_a_nan(n_h, parts):
     M.mla_destroy(h)
     for g, c in zip(res[1], res[0]):
         assert np.isfinite(c).all() and np.isnan(g[0]).all() and np.array_equal(g[1], c[1])
+
+
+@pytest.mark.parametrize("parts", [1, 0])
+@pytest.mark.parametrize("first", [1, 64, 256, 300, 700])
+@pytest.mark.parametrize("sh,page", SHAPES)
+def test_sparse_scores_that_overflow_to_minus_infinity(sh, page, first, parts):
+    """Tokens whose scores overflow to -inf draw nothing, whole tiles and pieces
+    of them at the front included; where no other token is left the row is
+    empty."""
+    s = Sparse(sh, (700, 1000, 1), 16, first, page)
+    s.sel = [list(range(11)), list(range(16)), [0]]
+    s.q[..., -1] = BIG
+    for r in s.rows:
+        r[:, -1] = 0
+    given = [r.copy() for r in s.rows]
+    for r in given:
+        r[:first, -1] = -BIG
+    kept, s.rows = s.rows, given
+    got = attend(s, parts)
+    scale = O.softmax_scale(sh["d_h"], sh["d_r"])
+    for b, r in enumerate(kept):
+        rest, q = r[first:].astype(np.float64), s.q[b].astype(np.float64)
+        want, lse = O.latent_attention(q, rest, d_c=sh["d_c"], scale=scale)
+        bo, bl = attention_bounds(sh, q, rest, scale, want, lse)
+        within(got[0][b], want, bo, f"ctx_lat of sequence {b}")
+        within(got[1][b], lse, bl, f"lse of sequence {b}")
