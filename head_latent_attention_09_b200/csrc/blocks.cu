@@ -173,6 +173,9 @@ __device__ __forceinline__ float log2_tokens(int j, int ctx) {
 // nothing (-inf - -inf is NaN), while a NaN, which no maximum shows, still
 // reaches the sum and with it every share of the head.
 __device__ __forceinline__ float minus_inf_to_0(float m) { return m == -CUDART_INF_F ? 0.f : m; }
+// The log-sum-exp that a head's shares are taken through; finite also for a head
+// with nothing but scores of -inf, whose shares then are 2^(-inf - 0) = 0.
+__device__ __forceinline__ float share_lse(float m, float sum) { return sum == 0.f ? 0.f : m + log2f(sum); }
 
 // CUDA cores, two launches: first x and the statistics, one warp per head, the
 // query row in registers (also bf16 beyond the tensor-core kernel's 4096 blocks).
@@ -360,7 +363,7 @@ __global__ void __launch_bounds__(kSThreads, 1)
           m = m2;
         }
         const bool real = ht * 128 + h < n_h;
-        const float lse = real ? m + log2f(sum) : 0.f;
+        const float lse = real ? share_lse(m, sum) : 0.f;
 #pragma unroll 1
         for (int g = 0; g < groups; ++g) {
           float v[32];
@@ -424,7 +427,7 @@ __global__ void __launch_bounds__(256) score_sum_kernel(const float *logits, con
         const float2 v = st[(long long)t * L.head_rows];
         sum += v.y * exp2f(v.x - minus_inf_to_0(m));
       }
-      lse[h] = m + log2f(sum);
+      lse[h] = share_lse(m, sum);
     }
   }
   __syncthreads();

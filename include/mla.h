@@ -530,7 +530,9 @@ int mla_block_scores_workspace_size(const mla_handle *handle, int B, int key_blo
  *   scores[b,j] = sum over heads i of softmax_j(x_i)_j
  * (the share of each head's attention that block j would draw if its tokens
  * had the block's mean row; a sequence's scores add up to n_h).  Blocks beyond
- * the sequence's get 0.  The scores are scaled as in mla_decode_attn
+ * the sequence's get 0.  A product that overflows to -inf draws nothing, and a
+ * head all of whose products do adds nothing to any block; a NaN or +inf makes
+ * every score of the sequence NaN.  The scores are scaled as in mla_decode_attn
  * (mla_set_rope_scaling included).
  *   q_abs [B, n_h, d_c+d_r], keys [B, key_blocks, d_c+d_r], scores float32 [B, key_blocks]
  * A sequence with more than key_blocks blocks is scored over the first

@@ -7,9 +7,9 @@ import torch
 
 import head_latent_attention_09_b200 as M
 from oracle import mla_oracle as O
-from tests.operators_harness import (LITE, TINY, V2, Cache, attention_bounds, dev, handle, host, ints, ok, shape, stored,
-                                     torch_type, within)
-from tests.test_gpu_blocks import Sparse
+from tests.operators_harness import (LITE, ODD, TINY, V2, Cache, attention_bounds, dev, handle, host, ints, ok, shape,
+                                     stored, torch_type, within)
+from tests.test_gpu_blocks import Sparse, compare_scores, scores_of
 
 pytestmark = pytest.mark.gpu
 
@@ -184,3 +184,25 @@ def test_sparse_scores_that_overflow_to_minus_infinity(sh, page, first, parts):
         bo, bl = attention_bounds(sh, q, rest, scale, want, lse)
         within(got[0][b], want, bo, f"ctx_lat of sequence {b}")
         within(got[1][b], lse, bl, f"lse of sequence {b}")
+
+
+@pytest.mark.parametrize("blocks", [1, 5, 300, 1100])
+@pytest.mark.parametrize("sh", [shape(LITE), shape(V2), shape(V2, n_h=200), shape(TINY), shape(ODD)])
+def test_block_scores_of_a_head_with_nothing_but_minus_infinity(sh, blocks):
+    """Such a head adds nothing to any block; where every head is one the scores
+    are zero."""
+    rng = np.random.default_rng(blocks)
+    ctx, n_h = [64 * blocks, 64 * blocks - 9], sh["n_h"]
+    keys = stored(sh, rng.standard_normal((2, blocks, sh["d_c"] + sh["d_r"])))
+    q = stored(sh, rng.standard_normal((2, n_h, sh["d_c"] + sh["d_r"])) * 0.7)
+    keys[:, :, 0], q[:, :, 0] = -BIG, 0
+    q[0, n_h - 2, 0] = BIG
+    q[1, :, 0] = BIG
+    h = handle(sh)
+    got = scores_of(sh, h, q, keys, ctx, blocks)
+    ok(h)
+    M.mla_destroy(h)
+    keys[:, :, 0] = 0
+    others = np.delete(q[0], n_h - 2, axis=0)
+    compare_scores({**sh, "n_h": n_h - 1}, got[:1], others[None], keys[:1], ctx[:1])
+    assert (got[1] == 0).all()
