@@ -337,6 +337,15 @@ __global__ void __launch_bounds__(256) attn_simt_kernel(AttnArgs a) {
       l = l * corr + (lane < kBatch ? pr : 0.f);
 #pragma unroll
       for (int j = 0; j < kO; ++j) o[j] *= corr;
+      // An infinity of a drafted row counts as zero behind its score of -inf (any
+      // other score of such a row makes its weight NaN).
+      if (kTree && __any_sync(0xffffffffu, s == -CUDART_INF_F && here && p0 + (lane & (kBatch - 1)) >= cached)) {
+#pragma unroll
+        for (int t = 0; t < kBatch; ++t)
+#pragma unroll
+          for (int j = 0; j < kO; ++j)
+            if (p0 + t >= cached && isinf(val[t][j])) val[t][j] = 0.f;
+      }
 #pragma unroll
       for (int t = 0; t < kBatch; ++t) {
         const float wt = __shfl_sync(0xffffffffu, pr, t);

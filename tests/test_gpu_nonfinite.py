@@ -10,6 +10,7 @@ from oracle import mla_oracle as O
 from tests.operators_harness import (LITE, ODD, TINY, V2, Cache, attention_bounds, dev, handle, host, ints, ok, shape,
                                      stored, torch_type, within)
 from tests.test_gpu_blocks import Sparse, compare_scores, scores_of
+from tests.test_gpu_tree import Tree
 
 pytestmark = pytest.mark.gpu
 
@@ -206,3 +207,20 @@ def test_block_scores_of_a_head_with_nothing_but_minus_infinity(sh, blocks):
     others = np.delete(q[0], n_h - 2, axis=0)
     compare_scores({**sh, "n_h": n_h - 1}, got[:1], others[None], keys[:1], ctx[:1])
     assert (got[1] == 0).all()
+
+
+@pytest.mark.parametrize("bad", [np.inf, -np.inf])
+@pytest.mark.parametrize("parts", [0, 3])
+@pytest.mark.parametrize("sh,page", [(shape(LITE), 0), (shape(LITE), 64), (shape(LITE), 32), (shape(TINY), 0),
+                                     (shape(ODD), 48)])
+def test_drafted_infinity_that_meets_minus_infinity(sh, page, parts, bad):
+    """An infinity of a drafted row's latent part whose scores are -inf counts as
+    zero for the tokens that attend it: theirs are the results without the row."""
+    t = Tree(sh, (60, 128, 300), 4, 8, page, [[1, 2, 5, 10]] * 3)
+    t.q[..., 0] = stored(sh, -np.sign(bad) * (np.abs(t.q[..., 0]) + 0.25))
+    rows = [r.copy() for r in t.rows]
+    for r, n in zip(rows, t.ctx):
+        r[n + 1, 0] = bad
+    got = t.run(parts, rows=rows)
+    t.bits = [[1, 0, 5, 8]] * 3
+    t.check(got)
