@@ -701,8 +701,8 @@ cudaError_t launch_tree_attn_simt(const AttnArgs &a, int P, bool fp32, cudaStrea
 // round by shuffles while the loads of kAhead pieces are in flight.  With
 // many rows one warp each fills the GPU; with few (long contexts split many
 // times) four warps a row and the loads in flight take the place of the missing
-// rows (4 sequences x 16 heads x 37 pieces: 32 -> 8 us; sixteen loads in flight
-// instead of eight took most of 3 us off that sparse attention's 20.6).
+// rows (256 rows of 37 pieces: 10.0 and 5.3 us; sixteen loads in flight instead
+// of eight took most of 3 us off a sparse attention of 20.6).
 template <typename T>
 __device__ __forceinline__ void store4(T *dst, float4 v);
 template <>
@@ -802,9 +802,12 @@ cudaError_t launch_combine(const mla_config &cfg, const char *ws, const WsLayout
   if (cfg.d_c % 4 == 0 && cfg.d_c <= 512 && ((uintptr_t)ctx_lat % (4 * esz)) == 0 &&
       ((uintptr_t)ws % 16) == 0) {
     const long long rows = (long long)B * cfg.n_h;
-    // Four warps a row while that is still at most about one resident set of
-    // warps (148 SMs x 64): more rows fill the GPU with one warp each.
-    const bool split = rows <= 2048;
+    // Four warps a row while their blocks are resident at once (two an SM: 592
+    // rows), or for rows of sixteen pieces, as long contexts have them; other rows
+    // do better with one warp each (one / four, us: 512 rows of 5 pieces 3.1 / 2.6,
+    // 1024 of 3 3.2 / 4.1, 2048 of 3 3.9 / 7.0, 1024 of 16 7.1 / 5.0, 2048 of 16
+    // 9.8 / 8.0).
+    const bool split = rows <= 592 || L.max_pieces - B >= 16ll * B;
     const unsigned blocks = (unsigned)((rows * (split ? 4 : 1) + 7) / 8);
     auto go = [&](auto kern, auto *out) {
       return launch_pdl(kern, dim3(blocks), dim3(256), 0, s, 1, ws, L, B, cfg.n_h, cfg.d_c, out, lse);
