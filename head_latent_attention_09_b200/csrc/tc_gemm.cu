@@ -625,7 +625,11 @@ int slice_chunks(int num_k_chunks, int ksplit, int bn) {
 // through the cluster (24 ns a column): of the choices that run in one wave, the
 // one with the least of both.  At d = 5120 (us, and what a tile as wide as the
 // tokens allow took): 64 tokens 32 columns x 8 6.9 (7.4), 256 tokens 64 x 6 9.1
-// (13.8), 512 tokens 128 x 6 11.1 (14.5), 768 tokens 128 x 4 13.1 (16.6).
+// (13.8), 512 tokens 128 x 6 11.1 (14.5), 768 tokens 128 x 4 13.1 (16.6).  Bulk
+// fills of 256 columns that would leave K whole are cut in two all the same: two
+// waves of half the length overlap better than one that leaves SMs idle, or than
+// two of whole ones (one / two slices, us: 4096 tokens of d = 2048 49.2 / 42.5, of
+// 5120 66.4 / 59.2, 8192 of 5120 115 / 93, 16384 164 / 153).
 void pick_append(int mtiles, long long N, int num_k_chunks, int *bn, int *ksplit) {
   const int sms = sm_count();
   double least = 1e30;
@@ -640,6 +644,7 @@ void pick_append(int mtiles, long long N, int num_k_chunks, int *bn, int *ksplit
         *ksplit = ks;
       }
     }
+  if (*bn == 256 && *ksplit <= 1 && num_k_chunks >= 4) *ksplit = 2;
 }
 
 int pick_bn(long long N) {

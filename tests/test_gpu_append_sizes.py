@@ -39,3 +39,10 @@ def test_append_of_many_tokens(sh, n):
     total = np.abs(x.astype(np.float64)) @ np.abs(np.concatenate([w["dkv"], w["kr"]]).astype(np.float64)).T
     total[:, sh["d_c"]:] = np.repeat(total[:, sh["d_c"]::2] + total[:, sh["d_c"] + 1::2], 2, axis=1)
     within(got[1:n + 1], want, (d * 2.0 ** -24 + 4e-6) * total + 2.0 ** -8 * np.abs(want) * 1.01, "rows")
+
+
+@pytest.mark.parametrize("n", [3000, 4097, 7500])
+@pytest.mark.parametrize("sh", [shape(LITE), shape(LITE, d_model=192), shape(LITE, d_model=256)])
+def test_append_of_a_long_prompt(sh, n):
+    """Tiles of 256 columns, with and without a K split."""
+    test_append_of_many_tokens(sh, n)
