@@ -426,7 +426,8 @@ __global__ void __launch_bounds__(128) combine_kernel(const char *ws, WsLayout L
 }
 
 // ---------------------------------------------------------------------------
-// cache append: one block per token; each warp computes a pair of features
+// cache append: one block per token; each warp computes a pair of features (of
+// the latent part, whose last pair is half one where d_c is odd, or rotary)
 // ---------------------------------------------------------------------------
 template <typename T>
 __global__ void __launch_bounds__(256) append_simt_kernel(
@@ -440,10 +441,12 @@ __global__ void __launch_bounds__(256) append_simt_kernel(
   __syncthreads();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int D = d_c + d_r;
-  const int f0 = 2 * (blockIdx.y * (blockDim.x >> 5) + warp);
+  const int unit = blockIdx.y * (blockDim.x >> 5) + warp, latent = (d_c + 1) / 2;
+  const int f0 = unit < latent ? 2 * unit : d_c + 2 * (unit - latent);
   if (f0 >= D) return;
+  const bool two = f0 + 1 != d_c;   // a second feature
   const T *w0 = f0 < d_c ? w_dkv + (long long)f0 * d : w_kr + (long long)(f0 - d_c) * d;
-  const T *w1 = w0 + d;
+  const T *w1 = two ? w0 + d : w0;
   float a0 = 0.f, a1 = 0.f;
   for (int k = lane; k < d; k += 32) {
     a0 += to_f(w0[k]) * sh[k];
@@ -464,7 +467,7 @@ __global__ void __launch_bounds__(256) append_simt_kernel(
   }
   if (rows_out) {
     rows_out[tok * D + f0] = a0;
-    rows_out[tok * D + f0 + 1] = a1;
+    if (two) rows_out[tok * D + f0 + 1] = a1;
     return;
   }
   const long long row = cache_row(b, p, cache_len, block_table, max_blocks, page_size);
@@ -473,7 +476,7 @@ __global__ void __launch_bounds__(256) append_simt_kernel(
     return;
   }
   cache[row * D + f0] = from_f<T>(a0);
-  cache[row * D + f0 + 1] = from_f<T>(a1);
+  if (two) cache[row * D + f0 + 1] = from_f<T>(a1);
 }
 
 // ---------------------------------------------------------------------------
@@ -879,8 +882,8 @@ cudaError_t launch_append_simt(const mla_config &cfg, const void *h, int B, int 
                                void *cache, long long cache_len, const int *block_table,
                                int max_blocks, const double *theta, unsigned *status,
                                cudaStream_t s, float *rows_out, const int *depth) {
-  const int D = cfg.d_c + cfg.d_r;
-  dim3 grid((unsigned)((long long)B * T), (D / 2 + 7) / 8);
+  const int units = (cfg.d_c + 1) / 2 + cfg.d_r / 2;
+  dim3 grid((unsigned)((long long)B * T), (units + 7) / 8);
   const size_t smem = sizeof(float) * cfg.d_model;
   if (smem > 48 * 1024) return cudaErrorNotSupported;
   if (cfg.dtype == MLA_FP32)

@@ -46,3 +46,10 @@ def test_append_of_many_tokens(sh, n):
 def test_append_of_a_long_prompt(sh, n):
     """Tiles of 256 columns, with and without a K split."""
     test_append_of_many_tokens(sh, n)
+
+
+@pytest.mark.parametrize("n", [1, 5])
+@pytest.mark.parametrize("sh", [shape(LITE, d_c=41, d_r=6, d_model=128), shape(LITE, d_c=1, d_r=2, d_model=64),
+                                shape((4, 32, 127, 16, 256, "fp32"))])
+def test_append_of_an_odd_latent_width(sh, n):
+    test_append_of_many_tokens(sh, n)
