@@ -499,3 +499,11 @@ def test_lengths_at_the_ends_of_the_integers(sh, n):
     assert n_sel.tolist() == [len(w) for w in want]
     assert sel.tolist() == want[0] + [-1] * (k - len(want[0])) + want[1]
     assert (guard[:2048] == 77).all() and (guard[2048 + 2 * k:] == 77).all()
+
+
+@pytest.mark.parametrize("page", [0, 64])
+def test_an_odd_latent_width(page):
+    sh = shape((3, 24, 41, 6, 128, "bf16"))
+    test_block_keys(sh, page)
+    test_block_scores(sh, 130)
+    Sparse(sh, (0, 1, 64, 65, 640, 1000, 1601), 5, 1, page).run()
