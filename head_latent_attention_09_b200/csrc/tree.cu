@@ -149,7 +149,8 @@ __global__ void __launch_bounds__(1024) tree_accept_kernel(U *cache, int units, 
   const long long cached = ctx_len[b];
   const long long cap = a.page_size ? (long long)a.max_blocks * a.page_size : a.cache_len;
   int n = n_path[b];
-  bool bad = n < 0 || n > T || cached < 0 || cached > cap;
+  // (a length past 2^31 - 1 could not be stored, however many tokens a table addresses)
+  bool bad = n < 0 || n > T || cached < 0 || cached > cap || cached + n > 0x7fffffffLL;
   if (bad) n = 0;
   __shared__ long long src[kTreeMaxDrafted], dst[kTreeMaxDrafted];
   for (int i = threadIdx.x; i < n; i += blockDim.x) {

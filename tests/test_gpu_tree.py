@@ -431,3 +431,35 @@ def test_rows_cut_into_more_pieces_than_a_warp_has_lanes(ctx, T, parts):
     sh = shape(LITE) if ctx != (2600,) else shape(TINY)
     t = Tree(sh, ctx, T, 4)
     t.check(t.run(parts))
+
+
+@pytest.mark.parametrize("n,fits", [(3, True), (4, False)])
+def test_accept_at_the_largest_length(n, fits):
+    """A table may address 2^31 tokens and more (here one page, again and again);
+    a length that an integer cannot hold is flagged and the sequence left."""
+    sh = shape((1, 8, 2, 2, 64, "fp32"))
+    h, T, ctx = handle(sh, 64), 4, 2 ** 31 - 4
+    blocks = 2 ** 25 + 1
+    table = torch.zeros(1, blocks, dtype=torch.int32, device="cuda")
+    pool = torch.arange(64 * 4, dtype=torch.float32, device="cuda").reshape(1, 64, 4)
+    before, new = pool.clone(), ints([0])
+    M.mla_tree_accept(h, pool, 1, table, blocks, ints([ctx]), ints([[0, 1, 2, 3]]), ints([n]), 1, T, new)
+    assert M.mla_get_device_status(h) == (M.MLA_OK if fits else M.MLA_ERR_DEVICE_BOUNDS)
+    assert new.tolist() == [ctx + n if fits else ctx]
+    assert torch.equal(pool, before)
+    M.mla_destroy(h)
+
+
+@pytest.mark.parametrize("page", [0, 16])
+def test_an_odd_latent_width(page):
+    sh = shape((3, 24, 41, 6, 128, "bf16"))
+    t = Tree(sh, (0, 1, 64, 130, 65), 6, 5, page)
+    t.check(t.run())
+    h = handle(sh, page)
+    cache = Cache(sh, t.rows, t.slots, page, t.rng)
+    new = ints([0] * 5)
+    M.mla_tree_accept(h, *cache.args, ints(t.ctx), ints([[1, 2, 5, 0, 0, 0]] * 5), ints([3] * 5), 5, 6, new)
+    ok(h)
+    M.mla_destroy(h)
+    for b, n in enumerate(t.ctx):
+        assert new[b].item() == n + 3 and np.array_equal(cache.rows(b, n + 6), O.tree_accept(t.rows[b], n, [1, 2, 5]))
