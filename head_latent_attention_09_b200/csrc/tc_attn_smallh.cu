@@ -694,7 +694,9 @@ __global__ void __launch_bounds__(Cfg<H, F8>::kThreads, 1)
         }
         {
           // P^T: K-major rows of 64 tokens (128 B) per head in two chunks,
-          // 16-byte units swizzled by row
+          // 16-byte units swizzled by row.  P is rounded to bf16 because the MMA
+          // takes both operands in one 16-bit type and V is bf16; the sum is of the
+          // unrounded values.
           uint8_t *pt = sP + (i & 1) * C::kPStride + (row >> 6) * H * 128;
           const int rr = row & 63, unit = rr >> 3, inunit = (rr & 7) * 2;
 #pragma unroll
