@@ -488,7 +488,8 @@ int mla_tree_attn(mla_handle *handle, const void *q_abs, const void *cache, long
  *           ctx_len itself
  * A sequence with an entry that does not rise, lies outside 0 .. T-1 or outside
  * the cache, with n_path outside 0 .. T, or with a new length above 2^31 - 1,
- * stays as it is (new_len = ctx_len) and sets MLA_ERR_DEVICE_BOUNDS in the status word.  T at most 64.
+ * stays as it is (new_len = ctx_len) and sets MLA_ERR_DEVICE_BOUNDS in the status
+ * word.  T at most 64.
  * Errors: INVALID_ARG, CUDA. */
 int mla_tree_accept(mla_handle *handle, void *cache, long long cache_len, const int *block_table,
                     int max_blocks_per_seq, const int *ctx_len, const int *path, const int *n_path, int B, int T,
